@@ -39,6 +39,33 @@ class PrologueParams(ctypes.Structure):
                 ("rope_base", ctypes.c_double), ("train_len", ctypes.c_double)]
 
 
+class Rope(ctypes.Structure):
+    """hils_rope (include/hils.h): the rotary position code of a model, made by rope()."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("freq", ctypes.c_double * 128)]
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+class QkParams(ctypes.Structure):
+    """hils_qk_params (include/hils.h)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "N", "Hq", "Hkv", "d", "pos0")] + [
+        (n, _Strides) for n in ("q_str", "k_str", "v_str", "qo_str", "ko_str", "dq_str",
+                                "dk_str")] + [
+        ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float)]
+
+
+class PagedParams(ctypes.Structure):
+    """hils_paged_params (include/hils.h)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "B", "Hq", "Hkv", "d", "n_pages",
+                                              "max_pages")] + [
+        ("c_str", _Strides), ("page_size", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 # every function the header declares, with its ctypes signature
 _P = ctypes.POINTER(Params)
 _V = ctypes.c_void_p
@@ -63,6 +90,22 @@ SIGNATURES = {
                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _V, _V,
                                         _V]),
     "hils_backward": (ctypes.c_int, [_P] + [_V] * 16 + [ctypes.c_size_t, _V]),
+    "hils_rope_init": (ctypes.c_int, [ctypes.POINTER(Rope)] + [ctypes.c_int32] * 3 +
+                       [ctypes.c_double] * 5),
+    "hils_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(QkParams), ctypes.POINTER(Rope)] +
+                          [_V] * 8),
+    "hils_qk_backward_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(QkParams)]),
+    "hils_qk_norm_rope_backward": (ctypes.c_int, [ctypes.POINTER(QkParams),
+                                                  ctypes.POINTER(Rope)] + [_V] * 12 +
+                                   [ctypes.c_size_t, _V]),
+    "hils_paged_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(PagedParams)]),
+    "hils_paged_plan": (ctypes.c_int, [ctypes.POINTER(PagedParams)] + [_V] * 12 +
+                        [ctypes.c_size_t, _V]),
+    "hils_paged_append": (ctypes.c_int, [ctypes.POINTER(QkParams), ctypes.POINTER(Rope),
+                                         ctypes.POINTER(PagedParams)] + [_V] * 11 +
+                          [ctypes.c_size_t, _V]),
+    "hils_paged_attn": (ctypes.c_int, [ctypes.POINTER(PagedParams)] + [_V] * 9 +
+                        [ctypes.c_size_t, _V]),
     "hils_chunk_attn": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V, _V]),
     "hils_fuse": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V]),
     "hils_workspace_init": (ctypes.c_int, [_V, ctypes.c_size_t, _V]),
@@ -403,6 +446,304 @@ def wait_check(polls, complete, ws, stream=None):
     """hils_wait_check: one bounded mbarrier wait on the device (see include/hils.h)."""
     _check(lib().hils_wait_check(int(polls), int(bool(complete)), _ptr(ws), ws.numel(),
                                  _stream(stream)), "hils_wait_check")
+
+
+# ------------------------------------------------- norms, rotary positions and the paged cache
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "hope": 4}
+
+
+def rope(rot_dim, *, layout="half", scaling="plain", base=10000.0, factor=1.0, train_len=0.0,
+         beta_fast=32.0, beta_slow=1.0, freq=None, mscale=None):
+    """The rotary position code of a model (hils_rope_init): pairs of the first rot_dim
+    dimensions, "half" or "interleaved", under the scaling rule "plain", "linear", "ntk", "yarn"
+    or "hope".  `freq` (rot_dim / 2 radians per position) and `mscale` replace the rule's."""
+    if layout not in _LAYOUTS or scaling not in _SCALINGS:
+        raise ValueError("layout is one of %s, scaling one of %s" %
+                         (sorted(_LAYOUTS), sorted(_SCALINGS)))
+    r = Rope()
+    _check(lib().hils_rope_init(ctypes.byref(r), rot_dim, _LAYOUTS[layout], _SCALINGS[scaling],
+                                base, factor, train_len, beta_fast, beta_slow), "hils_rope_init")
+    if freq is not None:
+        if len(freq) != rot_dim // 2:
+            raise ValueError("freq has %d entries, expected %d" % (len(freq), rot_dim // 2))
+        r.freq[:rot_dim // 2] = [float(f) for f in freq]
+    if mscale is not None:
+        r.mscale = float(mscale)
+    return r
+
+
+class _On:
+    """The device of `t` made current, and `stream` (default: that device's current stream) made
+    the stream that outputs and workspaces are allocated on; the caller's tensors are kept from
+    reuse until the work given to `stream` is done."""
+
+    def __init__(self, t, stream, used=()):
+        self.guards = ()
+        dev = t.device
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError("stream is on %s, the tensors on %s" % (stream.device, dev))
+            self.guards = (torch.cuda.stream(stream),)
+            for u in used:
+                if u is not None:
+                    u.record_stream(stream)
+        elif dev.index != torch.cuda.current_device():
+            self.guards = (torch.cuda.device(dev),)
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for g in self.guards:
+            g.__exit__(*exc)
+
+
+def _rows(t, name, dtype, shape, device, out=False):
+    """Checks a tensor whose last dimension is contiguous; the others by any strides (an
+    output's apart from one another)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device or not t.is_cuda:
+        raise ValueError("%s must live on the CUDA device %s (there is no CPU path)" %
+                         (name, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.numel():
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError("the last dimension of %s must be contiguous" % name)
+        if out:
+            # rows apart: from the innermost stride out, each dimension steps past the ones inside
+            span = t.shape[-1]
+            for st, n in sorted((t.stride(i), t.shape[i]) for i in range(t.dim() - 1)
+                                if t.shape[i] > 1):
+                if st < span:
+                    raise ValueError("rows of %s overlap" % name)
+                span = st * n
+    return t
+
+
+def _str3(t):
+    """Strides of the three outer dimensions of [.., .., .., d] (0 where a dimension is 1)."""
+    return _Strides(*[st if n > 1 else 0 for st, n in zip(t.stride()[:3], t.shape[:3])])
+
+
+def _ints(t, name, shape, device):
+    if t.device != device:
+        raise ValueError("%s must live on %s" % (name, device))
+    return _need(t, name, torch.int32, shape)
+
+
+def _qk_setup(q, k, w_q, w_k, pos, pos0, eps, norm):
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    if not x.is_cuda:
+        raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
+    dev, dt = x.device, x.dtype
+    B, _, N, d = x.shape
+    Hq = 0 if q is None else q.shape[1]
+    Hkv = 0 if k is None else k.shape[1]
+    p = QkParams(B=B, N=N, Hq=Hq, Hkv=Hkv, d=d, pos0=pos0, dtype=_dtype_code(dt),
+                 grad_dtype=_dtype_code(dt), norm=int(bool(norm)), eps=eps)
+    if q is not None:
+        p.q_str = _str3(_rows(q, "q", dt, (B, Hq, N, d), dev))
+    if k is not None:
+        p.k_str = _str3(_rows(k, "k", dt, (B, Hkv, N, d), dev))
+    for w, n in ((w_q, "w_q"), (w_k, "w_k")):
+        if w is not None:
+            _rows(w, n, dt, (d,), dev)
+    if pos is not None:
+        _ints(pos, "pos", (B, N), dev)
+    return p, dev, dt
+
+
+def qk_norm_rope(q, k, w_q, w_k, rope, *, pos=None, pos0=0, eps=1e-6, norm=True, q_out=None,
+                 k_out=None, stream=None):
+    """hils_qk_norm_rope: RMS norm (weights w_q, w_k [d] or None) and rotation of q [B,Hq,N,d] and
+    k [B,Hkv,N,d] (either may be None) at positions pos [B,N] int32 or pos0 + n.  Any strides over
+    a contiguous head dim; outputs default to contiguous tensors, q_out may be q.  norm=False
+    only rotates.  Returns (q_out, k_out)."""
+    p, dev, dt = _qk_setup(q, k, w_q, w_k, pos, pos0, eps, norm)
+    with _On(q if q is not None else k, stream, (q, k, w_q, w_k, pos, q_out, k_out)) as st:
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=dt, device=dev)
+            p.qo_str = _str3(_rows(q_out, "q_out", dt, q.shape, dev, out=True))
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=dt, device=dev)
+            p.ko_str = _str3(_rows(k_out, "k_out", dt, k.shape, dev, out=True))
+        _check(lib().hils_qk_norm_rope(ctypes.byref(p), ctypes.byref(rope), _ptr(q), _ptr(k),
+                                       _ptr(w_q), _ptr(w_k), _ptr(pos), _ptr(q_out), _ptr(k_out),
+                                       st), "hils_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, rope, *, pos=None, pos0=0, eps=1e-6,
+                          norm=True, dq=None, dk=None, stream=None):
+    """hils_qk_norm_rope_backward: the gradients of qk_norm_rope's inputs from those of its
+    outputs (fp32, as backward() returns them, or q's dtype; any strides).  Returns a dict of dq,
+    dk (in the gradients' dtype; dq may be dq_out) and dw_q, dw_k (fp32 [d], None where there is
+    no weight)."""
+    p, dev, dt = _qk_setup(q, k, w_q, w_k, pos, pos0, eps, norm)
+    gt = (dq_out if q is not None else dk_out).dtype
+    p.grad_dtype = _dtype_code(gt)
+    with _On(q if q is not None else k, stream,
+             (q, k, w_q, w_k, pos, dq_out, dk_out, dq, dk)) as st:
+        if q is not None:
+            p.qo_str = _str3(_rows(dq_out, "dq_out", gt, q.shape, dev))
+            if dq is None:
+                dq = torch.empty(q.shape, dtype=gt, device=dev)
+            p.dq_str = _str3(_rows(dq, "dq", gt, q.shape, dev, out=True))
+        if k is not None:
+            p.ko_str = _str3(_rows(dk_out, "dk_out", gt, k.shape, dev))
+            if dk is None:
+                dk = torch.empty(k.shape, dtype=gt, device=dev)
+            p.dk_str = _str3(_rows(dk, "dk", gt, k.shape, dev, out=True))
+        dw_q, dw_k = [None if w is None else torch.empty(w.shape, dtype=torch.float32, device=dev)
+                      for w in (w_q, w_k)]
+        ws = None
+        if dw_q is not None or dw_k is not None:
+            ws = torch.empty(int(lib().hils_qk_backward_workspace_size(ctypes.byref(p))),
+                             dtype=torch.uint8, device=dev)
+        _check(lib().hils_qk_norm_rope_backward(
+            ctypes.byref(p), ctypes.byref(rope), _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k),
+            _ptr(pos), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k),
+            _ptr(ws), 0 if ws is None else ws.numel(), st), "hils_qk_norm_rope_backward")
+    return {"dq": dq, "dk": dk, "dw_q": dw_q, "dw_k": dw_k}
+
+
+def _cache_params(K, V, T, B, Hq, max_pages, window=0, scale=0.0):
+    P, Hkv, ps, d = K.shape
+    _rows(K, "K", K.dtype, K.shape, K.device)
+    _rows(V, "V", K.dtype, K.shape, K.device)
+    c = PagedParams(T=T, B=B, Hq=Hq, Hkv=Hkv, d=d, n_pages=P, max_pages=max_pages, page_size=ps,
+                    window=window, dtype=_dtype_code(K.dtype), scale=float(scale))
+    c.c_str = _str3(K)
+    if list(_str3(V)) != list(c.c_str):
+        raise ValueError("K and V must have the same strides")
+    return c
+
+
+def paged_workspace(q=None, K=None, *, device=None, stream=None):
+    """A workspace for the paged calls (its status word, read with device_status, zeroed): of any
+    size for plan and append, with q [T,Hq,d] and K for attention of their heads too.  Calls that
+    overlap on the GPU (streams, replayed graphs) need one each."""
+    n = 256
+    if q is not None:
+        c = PagedParams(T=0, B=0, Hq=q.shape[1], Hkv=K.shape[1], d=q.shape[2], page_size=1)
+        n = int(lib().hils_paged_workspace_size(ctypes.byref(c)))
+        device = q.device
+    buf = torch.empty(n, dtype=torch.uint8, device=device)
+    with _On(buf, stream) as st:
+        _check(lib().hils_workspace_init(_ptr(buf), n, st), "hils_workspace_init")
+    return buf
+
+
+def paged_plan(kv_len, new_len, block_table, free_pages, n_free, *, page_size, T_cap,
+               kv_len_out=None, n_free_out=None, ws=None, stream=None):
+    """hils_paged_plan: the slots, positions and sequences of a step's new tokens, with the pages
+    they need taken from the free stack (free_pages [n_pages], n_free [1]) and entered in
+    block_table [B,max_pages] (in place).  T_cap bounds the tokens.  kv_len_out and n_free_out may
+    be kv_len and n_free.  Returns a dict: slot, pos, seq [T_cap], cu [B+1], kv_len [B],
+    n_free [1], all int32."""
+    B, M = block_table.shape
+    dev = block_table.device
+    _need(block_table, "block_table", torch.int32)
+    _ints(kv_len, "kv_len", (B,), dev)
+    _ints(new_len, "new_len", (B,), dev)
+    _ints(free_pages, "free_pages", (free_pages.numel(),), dev)
+    _ints(n_free, "n_free", (1,), dev)
+    c = PagedParams(T=T_cap, B=B, n_pages=free_pages.numel(), max_pages=M, page_size=page_size)
+    with _On(block_table, stream, (kv_len, new_len, block_table, free_pages, n_free, kv_len_out,
+                                   n_free_out, ws)) as st:
+        buf = torch.empty((3, max(T_cap, 0)), dtype=torch.int32, device=dev)
+        cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        kv_len_out = torch.empty_like(kv_len) if kv_len_out is None else \
+            _ints(kv_len_out, "kv_len_out", (B,), dev)
+        n_free_out = torch.empty_like(n_free) if n_free_out is None else \
+            _ints(n_free_out, "n_free_out", (1,), dev)
+        if ws is None:
+            ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+        slot, pos, seq = buf
+        _check(lib().hils_paged_plan(ctypes.byref(c), _ptr(kv_len), _ptr(new_len),
+                                     _ptr(block_table), _ptr(free_pages), _ptr(n_free),
+                                     _ptr(kv_len_out), _ptr(n_free_out), _ptr(cu), _ptr(slot),
+                                     _ptr(pos), _ptr(seq), _ptr(ws), ws.numel(), st),
+               "hils_paged_plan")
+    return {"slot": slot, "pos": pos, "seq": seq, "cu": cu, "kv_len": kv_len_out,
+            "n_free": n_free_out}
+
+
+def paged_append(q, k, v, w_q, w_k, rope, K, V, pos, slot, *, eps=1e-6, norm=True, q_out=None,
+                 ws=None, stream=None):
+    """hils_paged_append: qk_norm_rope of a step's tokens q [T,Hq,d], k, v [T,Hkv,d] (any strides)
+    at pos [T], keys and values written to slot [T] of the pools K, V [n_pages,Hkv,page_size,d]
+    (any strides; a [n_pages,page_size,Hkv,d] pool as its transpose).  Returns q_out, whose
+    padding rows (slot < 0) are left as they were (zero where it is allocated here)."""
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    tokens = lambda t: t.transpose(0, 1)[None]     # [T, H, d] as [1, H, T, d]
+    p, dev, dt = _qk_setup(tokens(q), tokens(k), w_q, w_k, None, 0, eps, norm)
+    p.v_str = _str3(tokens(_rows(v, "v", dt, (T, Hkv, d), dev)))
+    _rows(K, "K", dt, (K.shape[0], Hkv, K.shape[2], d), dev, out=True)
+    c = _cache_params(K, V, T, 0, Hq, 0)
+    _ints(pos, "pos", (T,), dev)
+    _ints(slot, "slot", (T,), dev)
+    with _On(q, stream, (q, k, v, w_q, w_k, K, V, pos, slot, q_out, ws)) as st:
+        if q_out is None:
+            q_out = torch.zeros((T, Hq, d), dtype=dt, device=dev)
+        p.qo_str = _str3(tokens(_rows(q_out, "q_out", dt, (T, Hq, d), dev, out=True)))
+        if ws is None:
+            ws = torch.zeros(256, dtype=torch.uint8, device=dev)
+        _check(lib().hils_paged_append(ctypes.byref(p), ctypes.byref(rope), ctypes.byref(c),
+                                       _ptr(q), _ptr(k), _ptr(v), _ptr(w_q), _ptr(w_k), _ptr(pos),
+                                       _ptr(slot), _ptr(q_out), _ptr(K), _ptr(V), _ptr(ws),
+                                       ws.numel(), st), "hils_paged_append")
+    return q_out
+
+
+def paged_attn(q, K, V, block_table, pos, *, seq=None, window=0, scale=0.0, out=None, lse=None,
+               ws=None, stream=None):
+    """hils_paged_attn: row t of q [T,Hq,d] attends to tokens 0 .. pos[t] (the last `window` of
+    them, if given) of sequence seq[t] (default t) in the pools K, V [n_pages,Hkv,page_size,d]
+    (any strides) through block_table [B,max_pages].  Returns (out [T,Hq,d], lse [T,Hq] fp32);
+    padding rows (seq < 0) are left as they were (zero where `out` is allocated here)."""
+    T, Hq, d = q.shape
+    dt = q.dtype
+    _need(q, "q")
+    dev = q.device
+    _rows(K, "K", dt, K.shape[:3] + (d,), dev)
+    B, M = block_table.shape
+    _ints(block_table, "block_table", (B, M), dev)
+    _ints(pos, "pos", (T,), dev)
+    if seq is not None:
+        _ints(seq, "seq", (T,), dev)
+    c = _cache_params(K, V, T, B, Hq, M, window, scale)
+    with _On(q, stream, (q, K, V, block_table, pos, seq, out, lse, ws)) as st:
+        new = torch.zeros if seq is not None else torch.empty
+        if out is None:
+            out = new((T, Hq, d), dtype=dt, device=dev)
+        if lse is None:
+            lse = new((T, Hq), dtype=torch.float32, device=dev)
+        if out.device != dev or lse.device != dev:
+            raise ValueError("out and lse must live on %s" % dev)
+        _need(out, "out", dt, (T, Hq, d))
+        _need(lse, "lse", torch.float32, (T, Hq))
+        if ws is None:
+            ws = torch.empty(max(256, int(lib().hils_paged_workspace_size(ctypes.byref(c)))),
+                             dtype=torch.uint8, device=dev)
+            ws[:256].zero_()
+        _check(lib().hils_paged_attn(ctypes.byref(c), _ptr(q), _ptr(K), _ptr(V),
+                                     _ptr(block_table), _ptr(seq), _ptr(pos), _ptr(out),
+                                     _ptr(lse), _ptr(ws), ws.numel(), st), "hils_paged_attn")
+    return out, lse
 
 
 def version():

@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "hils.h"
+#include "host.h"
 #include "kernels.h"
 
 #ifndef HILS_GIT_DESCRIBE
@@ -19,18 +20,12 @@
 namespace hils {
 namespace {
 
-constexpr size_t kAlign = 256;
-constexpr size_t kStatusBytes = 256;
 constexpr int kChunksPerSplit = 512;
 constexpr int64_t kDecodeMaxQueries = 16;
 constexpr int kStreamRows = 1024;  // landmark rows per streaming CTA (a ring of bulk copies)
 // decode rows from this many eligible chunks take the two-level top-K (group maxima)
 constexpr int64_t kTopkGroupMinChunks = 1024;
 
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct Plan {
   Dims D;
@@ -142,19 +137,6 @@ int n_stream_split(const Plan& P) {
   const int64_t s = (n_max + kStreamRows - 1) / kStreamRows;
   return (int)(s < 1 ? 1 : s);
 }
-
-hils_status check_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return HILS_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return HILS_ERR_CUDA;
-  if (major != 10 || minor != 0) return HILS_ERR_UNSUPPORTED;
-  return HILS_OK;
-}
-
-bool ok_ptr(const void* ptr, bool needed) { return !needed || (ptr && aligned16(ptr)); }
 
 }  // namespace
 }  // namespace hils

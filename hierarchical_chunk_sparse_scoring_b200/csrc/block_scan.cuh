@@ -1,0 +1,34 @@
+// Exclusive sum over a block of NT threads, one 64-bit value per thread.
+#pragma once
+
+#include <stdint.h>
+
+namespace hils {
+
+// sWarp: NT / 32 words of shared memory; `total` is the block's sum.  Called by every thread.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sWarp, int64_t& total) {
+  constexpr int NW = NT / 32;
+  static_assert(NT % 32 == 0 && NW <= 32, "whole warps, their sums in one warp");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sWarp[warp] = x;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const int64_t y = sWarp[w];
+    if (w < warp) before += y;
+    total += y;
+  }
+  __syncthreads();
+  return before + x - v;
+}
+
+}  // namespace hils

@@ -222,6 +222,176 @@ hils_status hils_hope_rotate(const hils_params* p, const hils_prologue_params* c
                              hils_stream_t stream);
 
 /*
+ * Around the attention: norms and rotary positions of queries and keys, and a paged cache.
+ *
+ * Rotary positions.  The first rot_dim dimensions of a head are rot_dim / 2 pairs: pair m is the
+ * dimensions (m, m + rot_dim/2) in the half layout and (2m, 2m + 1) in the interleaved one.  At
+ * position p a pair (a, b) becomes mscale (a cos t - b sin t, a sin t + b cos t) with
+ * t = p freq[m] radians, reduced in fp64; the other dimensions pass unchanged.  hils_rope_init
+ * fills freq with theta_m = base^(-2m/rot_dim) under one of these rules:
+ *   PLAIN   theta_m.
+ *   LINEAR  theta_m / factor (positions interpolated to a context factor times as long).
+ *   NTK     the base becomes base factor^(rot_dim/(rot_dim - 2)): the slowest pair is slowed by
+ *           factor, the fastest keeps its rate.
+ *   YARN    (Peng et al. 2023, "YaRN", section 3.2) by the turns r = train_len theta_m / (2 pi) a
+ *           pair makes over the trained length: g theta_m + (1 - g) theta_m / factor with
+ *           g = (r - beta_slow) / (beta_fast - beta_slow) clamped to [0, 1];
+ *           mscale = 0.1 ln(factor) + 1.
+ *   HOPE    theta_m where its period 2 pi / theta_m is at most train_len, else 0 (the rule of
+ *           hils_qcal_hope and hils_hope_rotate).
+ * A caller with another rule fills freq itself (mscale and freq finite).
+ */
+typedef enum { HILS_ROPE_HALF = 0, HILS_ROPE_INTERLEAVED = 1 } hils_rope_layout;
+typedef enum {
+  HILS_ROPE_PLAIN = 0,
+  HILS_ROPE_LINEAR = 1,
+  HILS_ROPE_NTK = 2,
+  HILS_ROPE_YARN = 3,
+  HILS_ROPE_HOPE = 4
+} hils_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim;   /* a multiple of 16, 0 (nothing turns) .. 256, at most the head dim */
+  int32_t layout;    /* hils_rope_layout */
+  float mscale;      /* multiplies the turned dimensions */
+  int32_t reserved;
+  double freq[128];  /* radians per position of pair m < rot_dim / 2 */
+} hils_rope;
+
+/* Host only.  base > 1, factor >= 1 (LINEAR, NTK, YARN), train_len > 0 and
+ * beta_fast > beta_slow (YARN); unused arguments are ignored.  mscale is set as stated above
+ * (1 except for YARN). */
+hils_status hils_rope_init(hils_rope* rope, int32_t rot_dim, int32_t layout, int32_t scaling,
+                           double base, double factor, double train_len, double beta_fast,
+                           double beta_slow);
+
+/*
+ * Norm and rotation of every query and key head in one pass: with x a head's d values at token n
+ * of sequence b,  r = 1 / sqrt(mean(x^2) + eps),  y = R_p (w * x r),  p the token's position.
+ * q, q_out [B, Hq, N, d] and k, k_out [B, Hkv, N, d] by strides (elements; batch, head, token;
+ * the head dim is contiguous), so heads-first and tokens-first tensors and slices of one fused
+ * projection are read in place; every stride and base a multiple of 16 bytes.  Output rows must
+ * not overlap; q_out may be q and k_out may be k (same strides).  w_q, w_k [d] in dtype, NULL for
+ * ones.  norm = 0: rotation only (w_q, w_k NULL).  pos [B, N] int32, or NULL for pos0 + n.
+ * Hq or Hkv may be 0.  d a multiple of 8 up to 256.  Sums, statistics and products are fp32, one
+ * rounding to dtype at the end.  Allocates nothing, needs no workspace, asynchronous on `stream`.
+ */
+typedef struct {
+  int64_t B, N, Hq, Hkv, d;
+  int64_t pos0;
+  int64_t q_str[3], k_str[3], v_str[3];   /* inputs (v: hils_paged_append) */
+  int64_t qo_str[3], ko_str[3];           /* outputs; backward: their gradients dq_out, dk_out */
+  int64_t dq_str[3], dk_str[3];           /* backward: gradients of q and k */
+  int32_t dtype;                          /* of q, k, v, w_q, w_k, q_out, k_out */
+  int32_t grad_dtype;                     /* backward: of dq_out, dk_out, dq, dk */
+  int32_t norm;
+  float eps;
+} hils_qk_params;
+
+hils_status hils_qk_norm_rope(const hils_qk_params* p, const hils_rope* rope, const void* q,
+                              const void* k, const void* w_q, const void* w_k,
+                              const int32_t* pos, void* q_out, void* k_out,
+                              hils_stream_t stream);
+
+/*
+ * Its gradients.  With g = R_p^T dy:  dw = sum over rows of g * x r (fp32, [d]),
+ * dx = r (w g - x r^2 mean(w g x)).  q, k, w_q, w_k, pos as given to hils_qk_norm_rope; dq_out
+ * and dk_out (qo_str, ko_str) and dq, dk (dq_str, dk_str) in grad_dtype, fp32 as hils_backward
+ * returns them or dtype; dq may be dq_out and dk may be dk_out (same strides).  dw_q, dw_k fp32,
+ * overwritten (zero when there are no rows), NULL to skip.  norm = 0: dx = g, no dw.  The weight
+ * sums are formed per block and joined in a fixed order (no atomics): the same call on the same
+ * device repeats bit for bit.  Workspace: hils_qk_backward_workspace_size bytes, 16-byte
+ * aligned, no initialisation needed.
+ */
+size_t hils_qk_backward_workspace_size(const hils_qk_params* p);
+hils_status hils_qk_norm_rope_backward(const hils_qk_params* p, const hils_rope* rope,
+                                       const void* q, const void* k, const void* w_q,
+                                       const void* w_k, const int32_t* pos, const void* dq_out,
+                                       const void* dk_out, void* dq, void* dk, float* dw_q,
+                                       float* dw_k, void* workspace, size_t workspace_bytes,
+                                       hils_stream_t stream);
+
+/*
+ * Paged cache.  K and V are pools of n_pages pages of page_size tokens, element
+ * (page, kv head, token, dim) at page c_str[0] + head c_str[1] + token c_str[2] + dim (both pools
+ * alike, in elements, multiples of 16 bytes), so [n_pages, Hkv, page_size, d] and
+ * [n_pages, page_size, Hkv, d] pools both serve.  block_table [B, max_pages] int32: token j of
+ * sequence b lies in page block_table[b][j / page_size]; its slot is page page_size +
+ * j % page_size.  n_pages page_size < 2^31.  What kernels read from device memory (lengths, page
+ * ids, slots, positions) is checked there: a bad value is skipped as stated at each call and
+ * HILS_ERR_DEVICE_CHECK is recorded in the workspace's status word (first 4 bytes, zeroed once
+ * with hils_workspace_init, read with hils_device_status).  Calls that overlap on the GPU must
+ * not share a workspace.
+ */
+typedef struct {
+  int64_t T;               /* tokens (rows) of the step */
+  int64_t B;               /* sequences: rows of the block table */
+  int64_t Hq, Hkv, d;
+  int64_t n_pages, max_pages;
+  int64_t c_str[3];
+  int32_t page_size;
+  int32_t window;          /* hils_paged_attn: the last `window` tokens are seen; 0: all */
+  int32_t dtype;
+  float scale;             /* <= 0: 1/sqrt(d) */
+} hils_paged_params;
+
+/* Bytes for any of the paged calls with these parameters (0 if they are invalid). */
+size_t hils_paged_workspace_size(const hils_paged_params* p);
+
+/*
+ * The plan of one step, on the GPU: sequence b holds kv_len[b] tokens and gets new_len[b] more.
+ * Its missing pages are taken from the top of the stack free_pages[0 .. n_free[0]) in order of
+ * (b, page) and entered in block_table (other entries are left as they are).  The new tokens are
+ * numbered in order of (b, position), token t < cu[B]:  seq[t] = b, pos[t] = its position,
+ * slot[t] = its slot; tokens cu[B] .. T - 1 get -1 in all three.  cu [B + 1] counts the tokens
+ * before each sequence; kv_len_out = kv_len + new_len and n_free_out the pages left, each may be
+ * its input (in place).  A sequence is refused (no tokens, no pages, length kept, recorded in the
+ * status word) if a length is negative, if it would outgrow max_pages, or if the tokens or pages
+ * asked for up to and including it exceed T or the free pages (one that needs no new page is not
+ * refused for pages).  A page id outside the pool gives slot -1 and is recorded.  Reads T, B,
+ * n_pages, max_pages, page_size of `p`; B <= 8192, T < 2^31.  Workspace: 256 bytes.
+ */
+hils_status hils_paged_plan(const hils_paged_params* p, const int32_t* kv_len,
+                            const int32_t* new_len, int32_t* block_table,
+                            const int32_t* free_pages, const int32_t* n_free,
+                            int32_t* kv_len_out, int32_t* n_free_out, int32_t* cu, int32_t* slot,
+                            int32_t* pos, int32_t* seq, void* workspace, size_t workspace_bytes,
+                            hils_stream_t stream);
+
+/*
+ * hils_qk_norm_rope for a step's tokens with the keys, and the values as they are, written to
+ * their slots of the cache: token t (B = 1, N = T of `p`; v by v_str) turns at pos[t]; its query
+ * goes to q_out row t, its key and value to slot[t].  A token with a negative slot is padding:
+ * nothing of it is written, its q_out row is left as it was.  So is one with a slot beyond the
+ * pool, which is recorded.  The slots of a call must be distinct.  `c` gives the cache (n_pages,
+ * page_size, c_str; T, Hq, Hkv, d and dtype as in `p`).  Workspace: 256 bytes.
+ */
+hils_status hils_paged_append(const hils_qk_params* p, const hils_rope* rope,
+                              const hils_paged_params* c, const void* q, const void* k,
+                              const void* v, const void* w_q, const void* w_k,
+                              const int32_t* pos, const int32_t* slot, void* q_out, void* K,
+                              void* V, void* workspace, size_t workspace_bytes,
+                              hils_stream_t stream);
+
+/*
+ * Attention of single tokens over the paged cache: row t (query q[t], q and out [T, Hq, d]
+ * contiguous) sees the tokens max(0, pos[t] - window + 1) .. pos[t] of sequence seq[t] (NULL:
+ * sequence t, T <= B), softmax over them with logits scale q.k; lse [T, Hq] fp32 (nullable) is
+ * their log-sum-exp.  Nothing else of the cache reaches the result, whatever it holds.  pos[t] =
+ * -1 is an empty row: out 0, lse -inf.  So is one with pos[t] < -1, pos[t] >= max_pages page_size
+ * or seq[t] >= B, which is recorded; tokens in a page outside the pool count as unseen and are
+ * recorded.  A row with seq[t] < 0 is padding, left as it was.  The work is split evenly over the
+ * SMs along the rows' lengths and joined in a fixed order, so a call repeats bit for bit (where a
+ * row is split, and with it its last bits, depends on the other rows' lengths); the launches do not depend on the lengths, so a step can be captured in a CUDA graph.  Supported:
+ * d = 64 or 128, G = Hq / Hkv <= 16.  bf16: products on the tensor cores, softmax weights rounded
+ * to bf16 for the product with V, sums fp32; fp32: all fp32.
+ */
+hils_status hils_paged_attn(const hils_paged_params* p, const void* q, const void* K,
+                            const void* V, const int32_t* block_table, const int32_t* seq,
+                            const int32_t* pos, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, hils_stream_t stream);
+
+/*
  * Backward pass: the gradients of L = sum dout . out + sum dlse . lse (out, lse as hils_forward
  * computes them) with respect to q, q_cal, K, V, k_lm and b_lm, with the selection topk_idx held
  * fixed.  The top-K is piecewise constant in its inputs and passes no gradient; the landmark keys
