@@ -6,16 +6,17 @@
 // flops for 2 d elements.
 //
 // Work split.  A unit is a (row, KV head); its tokens are cut into tiles of 16 (bf16) or 8 (fp32).
-// The tiles of all units in order (row, head, tile) form one list, and every CTA (one per SM, all
-// of its shared memory) takes an equal stretch of it, whatever the rows' lengths; CTAs sum the
-// rows' tile counts themselves, so nothing about the lengths is needed on the host.  A CTA writes
-// units that lie within its stretch; the part of a unit that crosses a boundary goes to the
-// workspace as (m, sum, unnormalised output), and the join kernel adds the parts in order.
+// All units in order (row, head) form one list in which a unit takes one place for its own cost
+// (queries, output) and one per tile.  Every CTA (one per SM, all of its shared memory) takes an
+// equal stretch of the list and every warp an equal stretch of its CTA's, whatever the rows'
+// lengths; CTAs sum the rows' tiles themselves, so nothing about the lengths is needed on the
+// host.  A warp walks its stretch with its own ring of cp.async stages, across unit boundaries,
+// and its own running maximum and sum, and writes units that lie within it: no block barrier
+// until every warp is done.  Then the parts (m, sum, O) of units cut by a warp boundary are added
+// in shared memory, and those of units cut by a CTA boundary go to the workspace, where the join
+// kernel adds them, always in the list's order.  The 128 KB a CTA has in flight cover the
+// latency of HBM; a tile's page id is read one tile ahead of its copy.
 //
-// Inside a CTA tile f of the stretch is warp f mod 8's, and each warp runs its own ring of cp.async
-// stages over its tiles, across unit boundaries, with its own running maximum and sum: no block
-// barrier while a unit lasts, two where one ends and the warps' results are added.  The 128 KB a
-// CTA has in flight cover the latency of HBM; a tile's page id is read one tile ahead of its copy.
 //   bf16  S^T = K Q^T and O^T += V^T P^T by m16n8k16 products: the tokens (then the head
 //         dimension) are the 16 rows, the G heads the 8 columns, so no row of a product is
 //         padding at G = 8 and P^T is S^T transposed in registers (movmatrix).
@@ -29,12 +30,12 @@ namespace hils {
 namespace {
 
 constexpr int kPaCtas = 148;      // CTAs at most (one per SM of 148)
-constexpr int kPaMinTiles = 8;    // tiles a CTA takes at least: one per warp
+constexpr int kPaMinWarp = 2;     // places of the list a warp takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The first unit of a CTA's stretch, for the join: offset of the stretch in the unit, the unit's
-// tiles, and the tiles per stretch (n = 0: no stretch).
+// The unit at the start of a CTA's stretch, for the join: the start's place in the unit, the
+// unit's places, and the places per stretch (n = 0: no stretch).
 struct PaRec {
   int64_t off, n, per;
   int32_t row, head;
@@ -65,6 +66,11 @@ struct PaRow {
   __device__ __forceinline__ int tiles() const {
     return hi > lo ? (hi - 1) / KT - lo / KT + 1 : 0;
   }
+  // places of one of its units in the list
+  template <int KT>
+  __device__ __forceinline__ int places() const {
+    return hi > lo ? tiles<KT>() + 1 : 0;
+  }
 };
 
 __device__ __forceinline__ PaRow pa_row(const PagedAttnArgs& a, int t, bool& bad) {
@@ -83,52 +89,57 @@ __device__ __forceinline__ PaRow pa_row(const PagedAttnArgs& a, int t, bool& bad
   return r;
 }
 
-// Where the CTA's stretch of the tile list begins.
-struct PaStart {
-  int64_t begin, end, per;   // tiles of the list
-  int64_t off;               // of the first unit before `begin`
+// Where a stretch of the list begins: the unit (row, head) holds place `begin` and starts at place
+// `unit` (begin >= total, the places of the list: no stretch).
+struct PaStretch {
+  int64_t begin, total, unit;
   int row, head;
 };
 
-template <int NT, int KT>
-__device__ __forceinline__ PaStart pa_schedule(const PagedAttnArgs& a, bool& bad) {
-  __shared__ int64_t sWarp[NT / 32];
-  __shared__ int64_t sOff;
-  __shared__ int sRow, sHead;
+// Places per CTA, and the stretches of this CTA's warps (in shared memory, sS [NW]).
+template <int NW, int KT>
+__device__ __forceinline__ int64_t pa_schedule(const PagedAttnArgs& a, PaStretch* sS, bool& bad) {
+  constexpr int NT = NW * 32;
+  __shared__ int64_t sWarp[NW];
   const int chunk = (a.T + NT - 1) / NT;
   const int t0 = threadIdx.x * chunk;
   const int t1 = t0 + chunk < a.T ? t0 + chunk : a.T;
   int64_t mine = 0;
-  for (int t = t0; t < t1; ++t) mine += pa_row(a, t, bad).tiles<KT>();
+  for (int t = t0; t < t1; ++t) mine += pa_row(a, t, bad).places<KT>();
   mine *= a.Hkv;
   int64_t total;
   int64_t at = block_scan<NT>(mine, sWarp, total);
-  PaStart s;
-  s.per = (total + gridDim.x - 1) / gridDim.x;
-  if (s.per < kPaMinTiles) s.per = kPaMinTiles;
-  s.begin = s.per * blockIdx.x;
-  s.end = s.begin + s.per < total ? s.begin + s.per : total;
-  if (s.begin < total && s.begin >= at && s.begin < at + mine) {
-    for (int t = t0; t < t1; ++t) {
-      const int64_t n = pa_row(a, t, bad).tiles<KT>();
-      if (s.begin < at + n * a.Hkv) {
-        sRow = t;
-        sHead = (int)((s.begin - at) / n);
-        sOff = (s.begin - at) - sHead * n;
-        break;
+  int64_t per_warp = (total + (int64_t)gridDim.x * NW - 1) / ((int64_t)gridDim.x * NW);
+  if (per_warp < kPaMinWarp) per_warp = kPaMinWarp;
+  const int64_t per = per_warp * NW, begin = per * blockIdx.x;
+  if (threadIdx.x < NW) {
+    sS[threadIdx.x].begin = begin + threadIdx.x * per_warp;
+    sS[threadIdx.x].total = total;
+  }
+  if (begin < at + mine && begin + per > at) {   // a stretch may begin among this thread's rows
+    int w = (int)(begin < at ? (at - begin + per_warp - 1) / per_warp : 0);
+    for (int t = t0; t < t1 && w < NW; ++t) {
+      const int64_t n = pa_row(a, t, bad).places<KT>();
+      for (; w < NW && begin + w * per_warp < at + n * a.Hkv; ++w) {
+        const int64_t head = (begin + w * per_warp - at) / n;
+        sS[w].row = t;
+        sS[w].head = (int)head;
+        sS[w].unit = at + head * n;
       }
       at += n * a.Hkv;
     }
   }
   __syncthreads();
-  s.row = sRow;
-  s.head = sHead;
-  s.off = sOff;
-  return s;
+  return per;
 }
 
 template <typename T>
 __device__ __forceinline__ void store_out(T* p, float v) { *p = Elem<T>::from_f(v); }
+
+// ln of the sum, from its maximum (base 2) and the sum relative to it.
+__device__ __forceinline__ float pa_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -180,16 +191,17 @@ struct PaShape {
   static constexpr int CH = ROW / 16;                       // its 16-byte pieces
   static constexpr int HALF = KT * ROW;                     // K (or V) of a tile
   static constexpr int STAGE = 2 * HALF;
-  // warps and the bytes of each one's ring: what fits beside the merge (G (D + 4) floats a warp)
+  // warps and the bytes of each one's ring: what fits beside the parts (G D floats a warp)
   static constexpr int NW = GM <= 4 || (GM <= 8 && sizeof(T) == 2) ? 8 : 6;
   static constexpr int ST = (GM <= 8 && NW == 6 ? 32768 : 24576) / STAGE;
   static constexpr int THREADS = NW * 32;
-  static constexpr int OS = D + 4;                          // floats per head of the merge
   static constexpr int SCRATCH = sizeof(T) == 2 ? 0 : KT * GM + GM;   // fp32: weights, factors
   static int smem(int G) {
-    return NW * ST * STAGE + NW * (G * OS + 2 * G + SCRATCH) * (int)sizeof(float);
+    return NW * ST * STAGE + NW * (G * D + 6 * G + SCRATCH) * (int)sizeof(float);
   }
-  static_assert(NW * (ST * STAGE + (GM * OS + 2 * GM + SCRATCH) * 4) <= 226 * 1024, "fits an SM");
+  static_assert(NW * (ST * STAGE + (GM * D + 6 * GM + SCRATCH) * 4) + 1024 <= 227 * 1024,
+                "fits an SM");
+  static_assert(GM * D * 4 <= ST * STAGE, "a part fits a warp's ring");
   static_assert(ST >= 3, "two tiles in flight while one is used");
   static_assert(CH == 8 || CH == 16 || CH == 32, "whole rows per copy");
 };
@@ -295,24 +307,58 @@ struct PaWarp<__nv_bfloat16, D, GM> {
       for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][i], a, p[nb][0], p[nb][1]);
     }
   }
+  // the sums over the tokens' lanes
+  __device__ __forceinline__ void close() {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1)
+          l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], w);
+  }
+  // a whole unit: out [G][D] and lse [G] (nullable)
+  __device__ __forceinline__ void emit(__nv_bfloat16* out, float* lse, int G, int lane) {
+    close();
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float inv[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int g = nb * 8 + (lane % 4) * 2 + e;
+        inv[e] = l[nb][e] > 0.f ? 1.f / l[nb][e] : l[nb][e];   // (0 and NaN stay)
+        if (lse && lane < 4 && g < G) lse[g] = pa_lse(m[nb][e], l[nb][e]);
+      }
+      const int g = nb * 8 + lane / 4;   // after the transposition: lane / 4 is the head
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __nv_bfloat162 w =
+              __floats2bfloat162_rn(o[nb][i][2 * h] * inv[0], o[nb][i][2 * h + 1] * inv[1]);
+          const uint32_t t = transpose8x8(*reinterpret_cast<const uint32_t*>(&w));
+          if (g < G)
+            *reinterpret_cast<uint32_t*>(out + g * D + i * 16 + h * 8 + (lane % 4) * 2) = t;
+        }
+    }
+  }
+  // a part of a unit, to shared memory
   __device__ __forceinline__ void finish(float* sO, float* sM, float* sL, int G, int lane) {
+    close();
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int g = nb * 8 + (lane % 4) * 2 + e;
-        float t = l[nb][e];
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
         if (g >= G) continue;
         if (lane < 4) {
           sM[g] = m[nb][e];
-          sL[g] = t;
+          sL[g] = l[nb][e];
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          sO[g * S::OS + i * 16 + lane / 4] = o[nb][i][e];
-          sO[g * S::OS + i * 16 + lane / 4 + 8] = o[nb][i][2 + e];
+          sO[g * D + i * 16 + lane / 4] = o[nb][i][e];
+          sO[g * D + i * 16 + lane / 4 + 8] = o[nb][i][2 + e];
         }
       }
   }
@@ -470,9 +516,31 @@ struct PaWarp<float, D, GM> {
       __syncwarp();   // the scratch is written again
     }
   }
-  __device__ __forceinline__ void finish(float* sO, float* sM, float* sL, int G, int lane) {
+  __device__ __forceinline__ void close() {
 #pragma unroll
     for (int w = 1; w < LPH; w <<= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  }
+  __device__ __forceinline__ void emit(float* out, float* lse, int G, int lane) {
+    close();
+    const int head = lane / LPH;
+    const float inv = l > 0.f ? 1.f / l : l;   // (0 and NaN stay)
+    if (lse && lane % LPH == 0 && head < G) lse[head] = pa_lse(m, l);
+#pragma unroll
+    for (int g = 0; g < GM; ++g) {
+      const float f = __shfl_sync(0xffffffffu, inv, g * LPH);
+      if (g < G) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) o[g][e] *= f;
+        if constexpr (EPL == 4)
+          *reinterpret_cast<float4*>(out + g * D + lane * EPL) =
+              make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
+        else
+          *reinterpret_cast<float2*>(out + g * D + lane * EPL) = make_float2(o[g][0], o[g][1]);
+      }
+    }
+  }
+  __device__ __forceinline__ void finish(float* sO, float* sM, float* sL, int G, int lane) {
+    close();
     const int head = lane / LPH;
     if (lane % LPH == 0 && head < G) {
       sM[head] = m;
@@ -482,48 +550,77 @@ struct PaWarp<float, D, GM> {
     for (int g = 0; g < GM; ++g) {
       if (g >= G) break;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) sO[g * S::OS + lane * EPL + e] = o[g][e];
+      for (int e = 0; e < EPL; ++e) sO[g * D + lane * EPL + e] = o[g][e];
     }
   }
 };
 
-// A warp's walk over the tiles of its CTA's stretch, for the copies: tile f of the stretch lies in
-// the unit part f0 .. f1 - 1, whose first tile is the row's tile t0.
-template <int KT>
+// A warp's walk over the units of its stretch: of the present one it takes tiles i0, i0 + step, ...
+// below i1 (of n; the row's tile t0 is the unit's first).  starts / ends: the stretch holds the
+// unit's first / last tile.
+template <int KT, int NW>
 struct PaWalk {
-  int64_t f, f0, f1, len;
-  int row, head;
-  int64_t t0;
+  int64_t end, unit;   // end of the stretch, place of the unit
+  int row, head, n, i0, i1, t0, step, turn;
+  bool starts, ends;
   PaRow R;
 
-  __device__ __forceinline__ void start(const PagedAttnArgs& a, const PaStart& s, int64_t at,
-                                        bool& bad) {
-    f = at;
-    f0 = 0;
-    len = s.end > s.begin ? s.end - s.begin : 0;
-    f1 = 0;
-    if (len == 0) return;
-    row = s.row;
-    head = s.head;
-    R = pa_row(a, row, bad);
-    t0 = R.lo / KT + s.off;
-    const int64_t n = R.template tiles<KT>() - s.off;
-    f1 = n < len ? n : len;
+  __device__ __forceinline__ void here(int64_t begin) {
+    n = R.template tiles<KT>();
+    t0 = R.lo / KT;
+    i0 = begin > unit ? (int)(begin - unit - 1) : 0;
+    i1 = end - unit - 1 < n ? (int)(end - unit - 1) : n;
+    starts = i0 == 0;
+    ends = i1 == n;
+    if (step > 1) {   // the tiles go round the warps; `turn` is this warp's distance to its next
+      const int mine = i0 + turn, count = i1 - i0;
+      turn = (turn + NW - count % NW) % NW;
+      i0 = mine;
+    }
   }
-  // to the next unit (there is one: f1 < len)
   __device__ __forceinline__ void next_unit(const PagedAttnArgs& a, bool& bad) {
-    f0 = f1;
+    unit += n + 1;
     if (++head == a.Hkv) {
       head = 0;
       do {
         ++row;
         R = pa_row(a, row, bad);
-      } while (R.template tiles<KT>() == 0);
+      } while (R.hi <= R.lo);
     }
-    t0 = R.lo / KT;
-    const int64_t n = R.template tiles<KT>();
-    f1 = f0 + n < len ? f0 + n : len;
+    here(unit);
   }
+  // the next unit has a tile in the stretch
+  __device__ __forceinline__ bool more() const { return unit + n + 2 < end; }
+  // to the first unit from here on with a tile for this warp; false if there is none
+  __device__ __forceinline__ bool settle(const PagedAttnArgs& a, bool& bad) {
+    while (i0 >= i1) {
+      if (!more()) return false;
+      next_unit(a, bad);
+    }
+    return true;
+  }
+  __device__ __forceinline__ bool next(const PagedAttnArgs& a, bool& bad) {
+    if (!more()) return false;
+    next_unit(a, bad);
+    return settle(a, bad);
+  }
+  __device__ __forceinline__ void open(const PagedAttnArgs& a, const PaStretch& s, int64_t e,
+                                       int st, int tu, bool& bad) {
+    end = e;
+    step = st;
+    turn = tu;
+    unit = s.unit;
+    row = s.row;
+    head = s.head;
+    R = pa_row(a, row, bad);
+    here(s.begin);
+  }
+};
+
+// A part of a unit left in shared memory by a warp.
+struct PaPart {
+  int row, head;      // row < 0: none
+  int starts, ends;   // it holds the unit's first / last tile
 };
 
 template <typename T, int D, int GM>
@@ -533,37 +630,69 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   constexpr int KT = S::KT, NW = S::NW, ST = S::ST, NT = S::THREADS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t sMask[NW][ST];
+  __shared__ PaStretch sStretch[NW];
+  __shared__ PaPart sPart[NW][2];
+  __shared__ uint32_t sMem[2 * NW];
+  __shared__ int sWhole[2 * NW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.G;
   uint8_t* ring = smem + warp * (ST * S::STAGE);
-  float* sO = reinterpret_cast<float*>(smem + NW * ST * S::STAGE);   // [NW][G][OS]
-  float* sM = sO + NW * G * S::OS;                                   // [NW][G]
-  float* sL = sM + NW * G;
-  float* scratch = sL + NW * G + warp * S::SCRATCH;
+  float* sO = reinterpret_cast<float*>(smem + NW * ST * S::STAGE);   // [NW][G][D]
+  float* sM = sO + NW * G * D;                                   // [NW][2][G]
+  float* sL = sM + NW * 2 * G;
+  float* sF = sL + NW * 2 * G;                                       // [NW][2][G]
+  float* scratch = sF + NW * 2 * G + warp * S::SCRATCH;
   bool bad = false;
-  const PaStart P = pa_schedule<NT, KT>(a, bad);
+  const int64_t per = pa_schedule<NW, KT>(a, sStretch, bad);
   const PaWs W = pa_carve(a.ws, G, D);
 
-  // ---- copies of this warp's tiles
-  PaWalk<KT> w;
-  w.start(a, P, warp, bad);
+  // ---- copies of this warp's tiles.  Where the CTA's stretch lies in at most two units its tiles
+  // go round the warps, so that the CTA reads consecutive rows (long rows: 563 us against 592 us
+  // with one stretch per warp, 8 rows of 120K tokens); else each warp has a stretch of its own
+  // and writes the units within it alone (fp32, 37 rows of up to 2048 tokens, 592 units: 53 us
+  // against 138 us with every unit shared by the warps)
+  PaWalk<KT, NW> w;
+  bool more = sStretch[0].begin < sStretch[0].total;
+  bool round = false;
+  const int64_t cta_end = sStretch[0].begin + per < sStretch[0].total ? sStretch[0].begin + per
+                                                                    : sStretch[0].total;
+  PaRec rec = {};
+  rec.per = per;
+  if (more) {
+    w.open(a, sStretch[0], cta_end, 1, 0, bad);
+    rec.off = sStretch[0].begin - w.unit;
+    rec.n = w.n + 1;
+    rec.row = w.row;
+    rec.head = w.head;
+    if (w.more()) w.next_unit(a, bad);
+    round = !w.more();
+  }
+  if (threadIdx.x == 0) W.rec[blockIdx.x] = rec;
+  const PaStretch& mine = sStretch[round ? 0 : warp];
+  more = mine.begin < mine.total;
+  const int64_t my_end = round ? cta_end
+                               : (mine.begin + per / NW < mine.total ? mine.begin + per / NW
+                                                                     : mine.total);
+  if (more) {
+    w.open(a, mine, my_end, round ? NW : 1, warp, bad);
+    more = w.settle(a, bad);
+  }
+  PaWalk<KT, NW> u = w;   // the same walk, for the products
+  bool go = more;
   int page = -1;
   bool want = false;
-  // the page of this lane's token of tile w.f (read here, used when the tile is copied)
+  // the page of this lane's token of tile w.i0 (read here, used when the tile is copied)
   auto look = [&]() {
-    want = false;
-    if (w.f >= w.len) return;
-    while (w.f >= w.f1) w.next_unit(a, bad);
-    const int64_t j = (w.t0 + w.f - w.f0) * KT + lane;
+    const int j = (w.t0 + w.i0) * KT + lane;
     want = lane < KT && j >= w.R.lo && j < w.R.hi;
-    if (want) page = a.table[w.R.seq * a.max_pages + (int)j / a.page_size];
+    if (want) page = a.table[w.R.seq * a.max_pages + j / a.page_size];
   };
   auto copy = [&](int stage) {
-    if (w.f < w.len) {
+    if (more) {
       int64_t at = -1;
       if (want) {
         if (page >= 0 && page < a.n_pages) {
-          const int j = (int)(w.t0 + w.f - w.f0) * KT + lane;
+          const int j = (w.t0 + w.i0) * KT + lane;
           at = page * a.cs[0] + w.head * a.cs[1] + (int64_t)(j % a.page_size) * a.cs[2];
         } else {
           bad = true;
@@ -583,48 +712,36 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
         copy16(dst, static_cast<const T*>(a.K) + eo, ro >= 0);
         copy16(dst + S::HALF, static_cast<const T*>(a.V) + eo, ro >= 0);
       }
-      w.f += NW;
-      look();
+      w.i0 += w.step;
+      if (w.i0 >= w.i1) more = w.next(a, bad);
+      if (more) look();
     }
     copy_commit();
   };
-  look();
+  if (more) look();
 #pragma unroll
   for (int s = 0; s < ST - 1; ++s) copy(s);
 
   // ---- rows that see nothing; what the join needs
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     const PaRow r = pa_row(a, t, bad);
-    if (r.seq < 0 || r.tiles<KT>() > 0) continue;
+    if (r.seq < 0 || r.hi > r.lo) continue;
     for (int e = threadIdx.x; e < a.Hq * D; e += NT)
       store_out(static_cast<T*>(a.out) + (int64_t)t * a.Hq * D + e, 0.f);
     if (a.lse)
       for (int h = threadIdx.x; h < a.Hq; h += NT) a.lse[(int64_t)t * a.Hq + h] = -INFINITY;
   }
-  PaWalk<KT> u;
-  u.start(a, P, warp, bad);
-  if (threadIdx.x == 0) {
-    PaRec rec = {};
-    rec.per = P.per;
-    if (u.len > 0) {
-      rec.off = P.off;
-      rec.n = u.R.template tiles<KT>();
-      rec.row = u.row;
-      rec.head = u.head;
-    }
-    W.rec[blockIdx.x] = rec;
-  }
+  if (threadIdx.x < 2 * NW) sPart[threadIdx.x / 2][threadIdx.x % 2].row = -1;
+  __syncthreads();
 
   // ---- the units of the stretch
   const float sc = a.scale * kLog2e;
   PaWarp<T, D, GM> c;
-  bool first = true;
-  int64_t off = P.off;
   int stage = 0;
-  while (u.f0 < u.len) {
+  while (go) {
     c.load(static_cast<const T*>(a.q) + ((int64_t)u.row * a.Hq + u.head * G) * D, G, lane);
     c.reset();
-    for (; u.f < u.f1; u.f += NW) {
+    for (int i = u.i0; i < u.i1; i += u.step) {
       copy_wait<ST - 2>();
       __syncwarp();   // every lane's copies have landed, and the stage before is read
       copy(stage == 0 ? ST - 1 : stage - 1);
@@ -632,77 +749,171 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
       c.tile(sK, sK + S::HALF, sMask[warp][stage], sc, lane, scratch);
       stage = stage + 1 == ST ? 0 : stage + 1;
     }
-    c.finish(sO + warp * G * S::OS, sM + warp * G, sL + warp * G, G, lane);
-    __syncthreads();
-    const int n = u.R.template tiles<KT>();
-    const bool whole = off == 0 && u.f1 - u.f0 == n;
-    const int part = blockIdx.x * 2 + (first ? 0 : 1);
-    for (int e = threadIdx.x; e < G * D; e += NT) {
-      const int g = e / D, i = e - g * D;
-      float M = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < NW; ++k) M = fmaxf(M, sM[k * G + g]);
-      float L = 0.f, O = 0.f;
-      if (M > -INFINITY) {
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-          const float f = exp2f(sM[k * G + g] - M);
-          L = fmaf(f, sL[k * G + g], L);
-          O = fmaf(f, sO[(k * G + g) * S::OS + i], O);
-        }
-      }
-      if (whole) {
-        const int64_t h = (int64_t)u.row * a.Hq + u.head * G + g;
-        store_out(static_cast<T*>(a.out) + h * D + i, L > 0.f ? O / L : 0.f);
-        if (a.lse && i == 0) a.lse[h] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-      } else {
-        W.o[((int64_t)part * G + g) * D + i] = O;
-        if (i == 0) {
-          W.ml[(part * G + g) * 2] = M;
-          W.ml[(part * G + g) * 2 + 1] = L;
-        }
-      }
+    const bool starts = u.starts, ends = u.ends;
+    const int row = u.row, head = u.head;
+    go = u.next(a, bad);
+    if (starts && ends && !round) {
+      const int64_t h = (int64_t)row * a.Hq + head * G;
+      c.emit(static_cast<T*>(a.out) + h * D, a.lse ? a.lse + h : nullptr, G, lane);
+    } else {
+      // the first part waits beside the rings, the last one in this warp's own, then unused
+      const int k = go ? 0 : 1;
+      __syncwarp();
+      c.finish(go ? sO + warp * G * D : reinterpret_cast<float*>(ring),
+               sM + (warp * 2 + k) * G, sL + (warp * 2 + k) * G, G, lane);
+      if (lane == 0) sPart[warp][k] = PaPart{row, head, starts, ends};
     }
-    __syncthreads();
-    first = false;
-    off = 0;
-    if (u.f1 >= u.len) break;
-    u.next_unit(a, bad);
   }
   copy_wait<0>();
   if (bad) record_status(a.status, kStatusDeviceCheck);
-}
+  __syncthreads();
 
-// Block (c, g): head g of the unit that boundary c = 1 .. ctas - 1 cuts, if c is the unit's first
-// boundary: the parts of CTAs c - 1, c, ... in that order.
-template <typename T, int D>
-__global__ void __launch_bounds__(D) paged_attn_join_kernel(const PagedAttnArgs a) {
-  const int c = blockIdx.x + 1, g = blockIdx.y, G = a.G;
-  const PaWs W = pa_carve(a.ws, G, D);
-  const PaRec r = W.rec[c];
-  if (r.n == 0 || r.off == 0 || r.off > r.per) return;
-  // the part before the boundary is CTA c - 1's first unit if its stretch begins with the unit
-  // (r.off == r.per) and otherwise its last
-  const int first = 2 * (c - 1) + (r.off == r.per ? 0 : 1);
-  const int parts = 1 + (int)((r.n - r.off + r.per - 1) / r.per);
-  float M = -INFINITY;
-  for (int k = 0; k < parts; ++k) {
-    const int part = k == 0 ? first : 2 * (c - 1 + k);
-    M = fmaxf(M, W.ml[(part * G + g) * 2]);
+  // ---- the parts.  Members of a part's unit as a bit mask, and each part's factor 2^(m - M)
+  if (threadIdx.x < 2 * NW) {
+    const int p = threadIdx.x;
+    const PaPart f = sPart[p / 2][p % 2];
+    uint32_t mem = 0;
+    int starts = 0, ends = 0;
+    if (f.row >= 0) {
+#pragma unroll
+      for (int o = 0; o < 2 * NW; ++o) {
+        const PaPart x = sPart[o / 2][o % 2];
+        if (x.row == f.row && x.head == f.head) {
+          mem |= 1u << o;
+          starts |= x.starts;
+          ends |= x.ends;
+        }
+      }
+    }
+    sMem[p] = mem;
+    sWhole[p] = starts && ends;
   }
-  float L = 0.f, O = 0.f;
-  if (M > -INFINITY) {
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const int part = k == 0 ? first : 2 * (c - 1 + k);
-      const float f = exp2f(W.ml[(part * G + g) * 2] - M);
-      L = fmaf(f, W.ml[(part * G + g) * 2 + 1], L);
-      O = fmaf(f, W.o[((int64_t)part * G + g) * D + threadIdx.x], O);
+  __syncthreads();
+  for (int x = threadIdx.x; x < 2 * NW * G; x += NT) {
+    const int p = x / G, g = x - p * G;
+    float M = -INFINITY;
+    for (uint32_t mem = sMem[p]; mem; mem &= mem - 1) M = fmaxf(M, sM[(__ffs(mem) - 1) * G + g]);
+    if (sMem[p]) sF[x] = exp2f(sM[x] - (M == -INFINITY ? 0.f : M));
+  }
+  __syncthreads();
+  for (int p = 0; p < 2 * NW; ++p) {
+    const uint32_t members = sMem[p];
+    if (members == 0 || __ffs(members) - 1 != p) continue;   // one round per unit
+    const PaPart f = sPart[p / 2][p % 2];
+    const bool whole = sWhole[p];
+    // the CTA's first unit goes to slot 0, another one that is cut to slot 1
+    const int slot = blockIdx.x * 2 + (f.row == rec.row && f.head == rec.head ? 0 : 1);
+    constexpr int EPT = (GM * D + NT - 1) / NT;   // elements per thread
+    float O[EPT], L[EPT];
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) O[k] = L[k] = 0.f;
+    for (uint32_t mem = members; mem; mem &= mem - 1) {
+      const int m = __ffs(mem) - 1;
+      const float* o = m % 2 ? reinterpret_cast<const float*>(smem + (m / 2) * (ST * S::STAGE))
+                             : sO + (m / 2) * G * D;
+#pragma unroll
+      for (int k = 0; k < EPT; ++k) {
+        const int e = threadIdx.x + k * NT, g = e / D, i = e - g * D;
+        if (g >= G) break;
+        const float r = sF[m * G + g];
+        L[k] = fmaf(r, sL[m * G + g], L[k]);
+        O[k] = fmaf(r, o[g * D + i], O[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      const int e = threadIdx.x + k * NT, g = e / D, i = e - g * D;
+      if (g >= G) break;
+      float M = -INFINITY;
+      if (i == 0)
+        for (uint32_t mem = members; mem; mem &= mem - 1)
+          M = fmaxf(M, sM[(__ffs(mem) - 1) * G + g]);
+      if (whole) {
+        const int64_t h = (int64_t)f.row * a.Hq + f.head * G + g;
+        store_out(static_cast<T*>(a.out) + h * D + i, L[k] == 0.f ? 0.f : O[k] / L[k]);
+        if (a.lse && i == 0) a.lse[h] = pa_lse(M, L[k]);
+      } else {
+        W.o[((int64_t)slot * G + g) * D + i] = O[k];
+        if (i == 0) {
+          W.ml[(slot * G + g) * 2] = M;
+          W.ml[(slot * G + g) * 2 + 1] = L[k];
+        }
+      }
     }
   }
+}
+
+// Block (x, g) adds head g of a cut unit: of the unit that boundary c = x + 1 cuts (BY_UNIT
+// false), or of unit x (true; fewer blocks when there are fewer units than boundaries).  A unit's
+// first boundary is the first behind one of its tiles (its place 0 is none); its parts are those
+// of CTAs c - 1, c, ..., added in that order by slices of the block, slice s taking every
+// (NT / D)th from the sth.
+template <typename T, int D, int NT, bool BY_UNIT>
+__global__ void __launch_bounds__(NT)
+    paged_attn_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
+  constexpr int NS = NT / D;
+  __shared__ float sF[kPaCtas], sRed[NT / 32], sO[NS][D];
+  __shared__ int sC;
+  const int g = blockIdx.y, G = a.G;
+  const PaWs W = pa_carve(a.ws, G, D);
+  int c = blockIdx.x + 1;
+  if constexpr (BY_UNIT) {
+    if (threadIdx.x == 0) sC = 0;
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t >= 1 && t < ctas) {
+      const PaRec r = W.rec[t];
+      if (r.n && (int64_t)r.row * a.Hkv + r.head == blockIdx.x && r.off > 1 && r.off <= r.per + 1)
+        sC = t;
+    }
+    __syncthreads();
+    c = sC;
+    if (c == 0) return;
+  }
+  const PaRec r = W.rec[c];
+  if (r.n == 0 || r.off <= 1 || r.off > r.per + 1) return;
+  // the part before the boundary is of CTA c - 1's first unit if its stretch begins in the unit
+  const int first = 2 * (c - 1) + (r.off >= r.per ? 0 : 1);
+  const int parts = 1 + (int)((r.n - r.off + r.per - 1) / r.per);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // factors and sum
+  float m = -INFINITY, l = 0.f;
+  const int k0 = threadIdx.x;   // (parts <= ctas <= 148 <= NT)
+  if (k0 < parts) {
+    const int part = k0 == 0 ? first : 2 * (c - 1 + k0);
+    const float2 t = *reinterpret_cast<const float2*>(W.ml + (part * G + g) * 2);
+    m = t.x;
+    l = t.y;
+  }
+  float M = warp_max(m);
+  if (lane == 0) sRed[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) M = fmaxf(M, sRed[w]);
+  const float f = k0 < parts ? exp2f(m - (M == -INFINITY ? 0.f : M)) : 0.f;
+  if (k0 < parts) sF[k0] = f;
+  l = warp_sum(f * l);
+  __syncthreads();
+  if (lane == 0) sRed[warp] = l;
+  __syncthreads();
+  float L = 0.f;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) L += sRed[w];
+  const int sl = threadIdx.x / D, i = threadIdx.x - sl * D;
+  float O = 0.f;
+#pragma unroll 8
+  for (int k = sl; k < parts; k += NS) {
+    const int part = k == 0 ? first : 2 * (c - 1 + k);
+    O = fmaf(sF[k], W.o[((int64_t)part * G + g) * D + i], O);
+  }
+  sO[sl][i] = O;
+  __syncthreads();
+  if (sl != 0) return;
+#pragma unroll
+  for (int s = 1; s < NS; ++s) O += sO[s][i];
   const int64_t h = (int64_t)r.row * a.Hq + r.head * G + g;
-  store_out(static_cast<T*>(a.out) + h * D + threadIdx.x, L > 0.f ? O / L : 0.f);
-  if (a.lse && threadIdx.x == 0) a.lse[h] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  store_out(static_cast<T*>(a.out) + h * D + i, L == 0.f ? 0.f : O / L);
+  if (a.lse && i == 0) a.lse[h] = pa_lse(M, L);
 }
 
 template <typename T, int D, int GM>
@@ -732,7 +943,12 @@ cudaError_t launch_both(const PagedAttnArgs& a, cudaStream_t st) {
         : a.G <= 8 ? launch_one<T, D, 8>(a, grid, st)
                    : launch_one<T, D, 16>(a, grid, st);
   if (e != cudaSuccess || grid < 2) return e;
-  paged_attn_join_kernel<T, D><<<dim3(grid - 1, a.G), D, 0, st>>>(a);
+  const int64_t units = (int64_t)a.T * a.Hkv;
+  if (units < grid - 1)
+    paged_attn_join_kernel<T, D, 1024, true>
+        <<<dim3((unsigned)units, a.G), 1024, 0, st>>>(a, grid);
+  else
+    paged_attn_join_kernel<T, D, 256, false><<<dim3(grid - 1, a.G), 256, 0, st>>>(a, grid);
   return cudaGetLastError();
 }
 
