@@ -28,6 +28,9 @@ struct PagedAttnArgs {
   float scale;
   int32_t* status;
   char* ws;           // the region after the status word
+  double inv_ctas;    // set by the launcher: 1 / CTAs, and the division by page_size
+  uint64_t page_mul;
+  int32_t page_shift;
 };
 bool paged_attn_supported(int64_t d, int64_t G);
 // Bytes of the attention's share of the workspace (after the status word).

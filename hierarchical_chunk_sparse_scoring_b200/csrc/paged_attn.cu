@@ -30,7 +30,7 @@ namespace hils {
 namespace {
 
 constexpr int kPaCtas = 148;      // CTAs at most (one per SM of 148)
-constexpr int kPaMinWarp = 2;     // places of the list a warp takes at least
+constexpr int kPaMinPer = 4;      // places of the list a CTA takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -96,9 +96,21 @@ struct PaStretch {
   int row, head;
 };
 
-// Places per CTA, and the stretches of this CTA's warps (in shared memory, sS [NW]).
+// x / n for 0 <= x < 65536 n: an estimate within one, put right.
+__device__ __forceinline__ int pa_head(int64_t x, int n) {
+  int64_t h = (int64_t)__fdividef((float)x, (float)n);
+  while (h * n > x) --h;
+  while ((h + 1) * n <= x) ++h;
+  return (int)h;
+}
+
+// Places per CTA and per warp, and where the stretches of this CTA's warps begin (in shared memory,
+// sS [NW]).
+struct PaPlan {
+  int64_t per, per_warp;
+};
 template <int NW, int KT>
-__device__ __forceinline__ int64_t pa_schedule(const PagedAttnArgs& a, PaStretch* sS, bool& bad) {
+__device__ __forceinline__ PaPlan pa_schedule(const PagedAttnArgs& a, PaStretch* sS, bool& bad) {
   constexpr int NT = NW * 32;
   __shared__ int64_t sWarp[NW];
   const int chunk = (a.T + NT - 1) / NT;
@@ -109,28 +121,33 @@ __device__ __forceinline__ int64_t pa_schedule(const PagedAttnArgs& a, PaStretch
   mine *= a.Hkv;
   int64_t total;
   int64_t at = block_scan<NT>(mine, sWarp, total);
-  int64_t per_warp = (total + (int64_t)gridDim.x * NW - 1) / ((int64_t)gridDim.x * NW);
-  if (per_warp < kPaMinWarp) per_warp = kPaMinWarp;
-  const int64_t per = per_warp * NW, begin = per * blockIdx.x;
+  // enough for every place (rounded up in doubles: 2^-53 of a total below 2^48 is no place)
+  PaPlan P;
+  P.per = (int64_t)((double)total * a.inv_ctas) + 1;
+  if (P.per < kPaMinPer) P.per = kPaMinPer;
+  P.per_warp = (P.per + NW - 1) / NW;
+  const int64_t begin = P.per * blockIdx.x;
   if (threadIdx.x < NW) {
-    sS[threadIdx.x].begin = begin + threadIdx.x * per_warp;
+    sS[threadIdx.x].begin = begin + threadIdx.x * P.per_warp;
     sS[threadIdx.x].total = total;
   }
-  if (begin < at + mine && begin + per > at) {   // a stretch may begin among this thread's rows
-    int w = (int)(begin < at ? (at - begin + per_warp - 1) / per_warp : 0);
+  if (begin < at + mine && begin + P.per > at) {   // a stretch may begin among this thread's rows
+    int w = 0;
+    while (w < NW && begin + w * P.per_warp < at) ++w;
     for (int t = t0; t < t1 && w < NW; ++t) {
-      const int64_t n = pa_row(a, t, bad).places<KT>();
-      for (; w < NW && begin + w * per_warp < at + n * a.Hkv; ++w) {
-        const int64_t head = (begin + w * per_warp - at) / n;
+      const int n = pa_row(a, t, bad).places<KT>();
+      const int64_t next = at + (int64_t)n * a.Hkv;
+      for (; w < NW && begin + w * P.per_warp < next; ++w) {
+        const int head = pa_head(begin + w * P.per_warp - at, n);
         sS[w].row = t;
-        sS[w].head = (int)head;
-        sS[w].unit = at + head * n;
+        sS[w].head = head;
+        sS[w].unit = at + (int64_t)head * n;
       }
-      at += n * a.Hkv;
+      at = next;
     }
   }
   __syncthreads();
-  return per;
+  return P;
 }
 
 template <typename T>
@@ -197,11 +214,11 @@ struct PaShape {
   static constexpr int THREADS = NW * 32;
   static constexpr int SCRATCH = sizeof(T) == 2 ? 0 : KT * GM + GM;   // fp32: weights, factors
   static int smem(int G) {
-    return NW * ST * STAGE + NW * (G * D + 6 * G + SCRATCH) * (int)sizeof(float);
+    return NW * ST * STAGE + NW * (G * D + 4 * G + SCRATCH) * (int)sizeof(float);
   }
-  static_assert(NW * (ST * STAGE + (GM * D + 6 * GM + SCRATCH) * 4) + 1024 <= 227 * 1024,
+  static_assert(NW * (ST * STAGE + (GM * D + 4 * GM + SCRATCH) * 4) + 1024 <= 227 * 1024,
                 "fits an SM");
-  static_assert(GM * D * 4 <= ST * STAGE, "a part fits a warp's ring");
+  static_assert((GM * D + 6 * NW * GM) * 4 <= ST * STAGE, "a part and the join fit a warp's ring");
   static_assert(ST >= 3, "two tiles in flight while one is used");
   static_assert(CH == 8 || CH == 16 || CH == 32, "whole rows per copy");
 };
@@ -633,17 +650,15 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   __shared__ PaStretch sStretch[NW];
   __shared__ PaPart sPart[NW][2];
   __shared__ uint32_t sMem[2 * NW];
-  __shared__ int sWhole[2 * NW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.G;
   uint8_t* ring = smem + warp * (ST * S::STAGE);
   float* sO = reinterpret_cast<float*>(smem + NW * ST * S::STAGE);   // [NW][G][D]
   float* sM = sO + NW * G * D;                                   // [NW][2][G]
   float* sL = sM + NW * 2 * G;
-  float* sF = sL + NW * 2 * G;                                       // [NW][2][G]
-  float* scratch = sF + NW * 2 * G + warp * S::SCRATCH;
+  float* scratch = sL + NW * 2 * G + warp * S::SCRATCH;
   bool bad = false;
-  const int64_t per = pa_schedule<NW, KT>(a, sStretch, bad);
+  const PaPlan P = pa_schedule<NW, KT>(a, sStretch, bad);
   const PaWs W = pa_carve(a.ws, G, D);
 
   // ---- copies of this warp's tiles.  Where the CTA's stretch lies in at most two units its tiles
@@ -654,10 +669,10 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   PaWalk<KT, NW> w;
   bool more = sStretch[0].begin < sStretch[0].total;
   bool round = false;
-  const int64_t cta_end = sStretch[0].begin + per < sStretch[0].total ? sStretch[0].begin + per
-                                                                    : sStretch[0].total;
+  const int64_t total = sStretch[0].total;
+  const int64_t cta_end = sStretch[0].begin + P.per < total ? sStretch[0].begin + P.per : total;
   PaRec rec = {};
-  rec.per = per;
+  rec.per = P.per;
   if (more) {
     w.open(a, sStretch[0], cta_end, 1, 0, bad);
     rec.off = sStretch[0].begin - w.unit;
@@ -669,10 +684,9 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   }
   if (threadIdx.x == 0) W.rec[blockIdx.x] = rec;
   const PaStretch& mine = sStretch[round ? 0 : warp];
-  more = mine.begin < mine.total;
-  const int64_t my_end = round ? cta_end
-                               : (mine.begin + per / NW < mine.total ? mine.begin + per / NW
-                                                                     : mine.total);
+  more = mine.begin < cta_end;
+  const int64_t my_end =
+      round || mine.begin + P.per_warp > cta_end ? cta_end : mine.begin + P.per_warp;
   if (more) {
     w.open(a, mine, my_end, round ? NW : 1, warp, bad);
     more = w.settle(a, bad);
@@ -681,11 +695,13 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   bool go = more;
   int page = -1;
   bool want = false;
+  // j / page_size (see launch_both)
+  auto page_of = [&](int j) { return (int)((uint64_t)(uint32_t)j * a.page_mul >> a.page_shift); };
   // the page of this lane's token of tile w.i0 (read here, used when the tile is copied)
   auto look = [&]() {
     const int j = (w.t0 + w.i0) * KT + lane;
     want = lane < KT && j >= w.R.lo && j < w.R.hi;
-    if (want) page = a.table[w.R.seq * a.max_pages + j / a.page_size];
+    if (want) page = a.table[w.R.seq * a.max_pages + page_of(j)];
   };
   auto copy = [&](int stage) {
     if (more) {
@@ -693,7 +709,8 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
       if (want) {
         if (page >= 0 && page < a.n_pages) {
           const int j = (w.t0 + w.i0) * KT + lane;
-          at = page * a.cs[0] + w.head * a.cs[1] + (int64_t)(j % a.page_size) * a.cs[2];
+          at = page * a.cs[0] + w.head * a.cs[1] +
+               (int64_t)(j - page_of(j) * a.page_size) * a.cs[2];
         } else {
           bad = true;
         }
@@ -768,76 +785,75 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   if (bad) record_status(a.status, kStatusDeviceCheck);
   __syncthreads();
 
-  // ---- the parts.  Members of a part's unit as a bit mask, and each part's factor 2^(m - M)
-  if (threadIdx.x < 2 * NW) {
-    const int p = threadIdx.x;
+  // ---- the parts, unit by unit: their members as a bit mask, each one's factor 2^(m - M), and
+  // the unit's maximum M and sum (all behind the last part of the first ring)
+  float* sF = reinterpret_cast<float*>(smem) + G * D;   // [NW][2][G]
+  float* sUM = sF + NW * 2 * G;                         // [NW][2][G], at the unit's first member
+  float* sUL = sUM + NW * 2 * G;
+  for (int x = threadIdx.x; x < 2 * NW * G; x += NT) {
+    const int p = x / G, g = x - p * G;
     const PaPart f = sPart[p / 2][p % 2];
     uint32_t mem = 0;
     int starts = 0, ends = 0;
-    if (f.row >= 0) {
+    float M = -INFINITY;
 #pragma unroll
-      for (int o = 0; o < 2 * NW; ++o) {
-        const PaPart x = sPart[o / 2][o % 2];
-        if (x.row == f.row && x.head == f.head) {
-          mem |= 1u << o;
-          starts |= x.starts;
-          ends |= x.ends;
-        }
+    for (int o = 0; o < 2 * NW; ++o) {
+      const PaPart y = sPart[o / 2][o % 2];
+      if (f.row >= 0 && y.row == f.row && y.head == f.head) {
+        mem |= 1u << o;
+        starts |= y.starts;
+        ends |= y.ends;
+        M = fmaxf(M, sM[o * G + g]);
       }
     }
-    sMem[p] = mem;
-    sWhole[p] = starts && ends;
+    if (g == 0) sMem[p] = mem && __ffs(mem) - 1 == p ? mem | (starts && ends ? 1u << 31 : 0u) : 0u;
+    if (mem) {
+      const float base = M == -INFINITY ? 0.f : M;
+      sF[x] = exp2f(sM[x] - base);
+      sUM[x] = M;
+      float L = 0.f;
+#pragma unroll
+      for (int o = 0; o < 2 * NW; ++o)
+        if (mem >> o & 1) L = fmaf(exp2f(sM[o * G + g] - base), sL[o * G + g], L);
+      sUL[x] = L;
+    }
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < 2 * NW * G; x += NT) {
-    const int p = x / G, g = x - p * G;
-    float M = -INFINITY;
-    for (uint32_t mem = sMem[p]; mem; mem &= mem - 1) M = fmaxf(M, sM[(__ffs(mem) - 1) * G + g]);
-    if (sMem[p]) sF[x] = exp2f(sM[x] - (M == -INFINITY ? 0.f : M));
-  }
-  __syncthreads();
-  for (int p = 0; p < 2 * NW; ++p) {
-    const uint32_t members = sMem[p];
-    if (members == 0 || __ffs(members) - 1 != p) continue;   // one round per unit
+  const uint32_t firsts = __ballot_sync(0xffffffffu, lane < 2 * NW && sMem[lane % (2 * NW)] != 0);
+  constexpr int Q = D / 4;   // a thread adds four dimensions of a head
+  for (uint32_t left = firsts; left; left &= left - 1) {
+    const int p = __ffs(left) - 1;
+    const uint32_t mem = sMem[p];
+    const bool whole = mem >> 31;
     const PaPart f = sPart[p / 2][p % 2];
-    const bool whole = sWhole[p];
     // the CTA's first unit goes to slot 0, another one that is cut to slot 1
     const int slot = blockIdx.x * 2 + (f.row == rec.row && f.head == rec.head ? 0 : 1);
-    constexpr int EPT = (GM * D + NT - 1) / NT;   // elements per thread
-    float O[EPT], L[EPT];
+    for (int e = threadIdx.x; e < G * Q; e += NT) {
+      const int g = e / Q, i = 4 * (e % Q);
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < EPT; ++k) O[k] = L[k] = 0.f;
-    for (uint32_t mem = members; mem; mem &= mem - 1) {
-      const int m = __ffs(mem) - 1;
-      const float* o = m % 2 ? reinterpret_cast<const float*>(smem + (m / 2) * (ST * S::STAGE))
-                             : sO + (m / 2) * G * D;
-#pragma unroll
-      for (int k = 0; k < EPT; ++k) {
-        const int e = threadIdx.x + k * NT, g = e / D, i = e - g * D;
-        if (g >= G) break;
-        const float r = sF[m * G + g];
-        L[k] = fmaf(r, sL[m * G + g], L[k]);
-        O[k] = fmaf(r, o[g * D + i], O[k]);
+      for (int o = 0; o < 2 * NW; ++o) {
+        if (!(mem >> o & 1)) continue;
+        const float r = sF[o * G + g];
+        const float4 v = *reinterpret_cast<const float4*>(
+            (o % 2 ? reinterpret_cast<const float*>(smem + (o / 2) * (ST * S::STAGE))
+                   : sO + (o / 2) * G * D) + g * D + i);
+        O.x = fmaf(r, v.x, O.x);
+        O.y = fmaf(r, v.y, O.y);
+        O.z = fmaf(r, v.z, O.z);
+        O.w = fmaf(r, v.w, O.w);
       }
-    }
-#pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      const int e = threadIdx.x + k * NT, g = e / D, i = e - g * D;
-      if (g >= G) break;
-      float M = -INFINITY;
-      if (i == 0)
-        for (uint32_t mem = members; mem; mem &= mem - 1)
-          M = fmaxf(M, sM[(__ffs(mem) - 1) * G + g]);
+      const float L = sUL[p * G + g], M = sUM[p * G + g];
       if (whole) {
         const int64_t h = (int64_t)f.row * a.Hq + f.head * G + g;
-        store_out(static_cast<T*>(a.out) + h * D + i, L[k] == 0.f ? 0.f : O[k] / L[k]);
-        if (a.lse && i == 0) a.lse[h] = pa_lse(M, L[k]);
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        float v[4] = {O.x * inv, O.y * inv, O.z * inv, O.w * inv};
+        Elem<T>::store4(static_cast<T*>(a.out) + h * D + i, v);
+        if (a.lse && i == 0) a.lse[h] = pa_lse(M, L);
       } else {
-        W.o[((int64_t)slot * G + g) * D + i] = O[k];
-        if (i == 0) {
-          W.ml[(slot * G + g) * 2] = M;
-          W.ml[(slot * G + g) * 2 + 1] = L[k];
-        }
+        *reinterpret_cast<float4*>(W.o + ((int64_t)slot * G + g) * D + i) = O;
+        if (i == 0)
+          *reinterpret_cast<float2*>(W.ml + (slot * G + g) * 2) = make_float2(M, L);
       }
     }
   }
@@ -934,21 +950,29 @@ cudaError_t launch_both(const PagedAttnArgs& a, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int grid = sms < kPaCtas ? sms : kPaCtas;
+  PagedAttnArgs b = a;
+  b.inv_ctas = 1.0 / grid;
+  // j / page_size as j mul >> shift, exact below 2^31: with 2^s >= page_size and
+  // mul = ceil(2^(31+s) / page_size) the error j (mul page_size - 2^(31+s)) stays below 2^(31+s)
+  int s = 0;
+  while (((int64_t)1 << s) < a.page_size) ++s;
+  b.page_mul = (((uint64_t)1 << (31 + s)) + a.page_size - 1) / a.page_size;
+  b.page_shift = 31 + s;
   // (bf16: up to 8 heads are the columns of one product, so one bound serves them)
   if constexpr (sizeof(T) == 2)
-    e = a.G <= 8 ? launch_one<T, D, 8>(a, grid, st) : launch_one<T, D, 16>(a, grid, st);
+    e = a.G <= 8 ? launch_one<T, D, 8>(b, grid, st) : launch_one<T, D, 16>(b, grid, st);
   else
-    e = a.G <= 1   ? launch_one<T, D, 1>(a, grid, st)
-        : a.G <= 4 ? launch_one<T, D, 4>(a, grid, st)
-        : a.G <= 8 ? launch_one<T, D, 8>(a, grid, st)
-                   : launch_one<T, D, 16>(a, grid, st);
+    e = a.G <= 1   ? launch_one<T, D, 1>(b, grid, st)
+        : a.G <= 4 ? launch_one<T, D, 4>(b, grid, st)
+        : a.G <= 8 ? launch_one<T, D, 8>(b, grid, st)
+                   : launch_one<T, D, 16>(b, grid, st);
   if (e != cudaSuccess || grid < 2) return e;
   const int64_t units = (int64_t)a.T * a.Hkv;
   if (units < grid - 1)
     paged_attn_join_kernel<T, D, 1024, true>
-        <<<dim3((unsigned)units, a.G), 1024, 0, st>>>(a, grid);
+        <<<dim3((unsigned)units, a.G), 1024, 0, st>>>(b, grid);
   else
-    paged_attn_join_kernel<T, D, 256, false><<<dim3(grid - 1, a.G), 256, 0, st>>>(a, grid);
+    paged_attn_join_kernel<T, D, 256, false><<<dim3(grid - 1, a.G), 256, 0, st>>>(b, grid);
   return cudaGetLastError();
 }
 
