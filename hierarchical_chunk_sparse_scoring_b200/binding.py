@@ -7,6 +7,7 @@ raises.
 """
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -92,20 +93,14 @@ SIGNATURES = {
     "hils_backward": (ctypes.c_int, [_P] + [_V] * 16 + [ctypes.c_size_t, _V]),
     "hils_rope_init": (ctypes.c_int, [ctypes.POINTER(Rope)] + [ctypes.c_int32] * 3 +
                        [ctypes.c_double] * 5),
-    "hils_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(QkParams), ctypes.POINTER(Rope)] +
-                          [_V] * 8),
-    "hils_qk_backward_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(QkParams)]),
-    "hils_qk_norm_rope_backward": (ctypes.c_int, [ctypes.POINTER(QkParams),
-                                                  ctypes.POINTER(Rope)] + [_V] * 12 +
-                                   [ctypes.c_size_t, _V]),
-    "hils_paged_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(PagedParams)]),
-    "hils_paged_plan": (ctypes.c_int, [ctypes.POINTER(PagedParams)] + [_V] * 12 +
-                        [ctypes.c_size_t, _V]),
-    "hils_paged_append": (ctypes.c_int, [ctypes.POINTER(QkParams), ctypes.POINTER(Rope),
-                                         ctypes.POINTER(PagedParams)] + [_V] * 11 +
-                          [ctypes.c_size_t, _V]),
-    "hils_paged_attn": (ctypes.c_int, [ctypes.POINTER(PagedParams)] + [_V] * 9 +
-                        [ctypes.c_size_t, _V]),
+    # (parameter structures of these calls: packed bytes or a structure by reference)
+    "hils_qk_norm_rope": (ctypes.c_int, [_V] * 10),
+    "hils_qk_backward_workspace_size": (ctypes.c_size_t, [_V]),
+    "hils_qk_norm_rope_backward": (ctypes.c_int, [_V] * 14 + [ctypes.c_size_t, _V]),
+    "hils_paged_workspace_size": (ctypes.c_size_t, [_V]),
+    "hils_paged_plan": (ctypes.c_int, [_V] * 13 + [ctypes.c_size_t, _V]),
+    "hils_paged_append": (ctypes.c_int, [_V] * 14 + [ctypes.c_size_t, _V]),
+    "hils_paged_attn": (ctypes.c_int, [_V] * 10 + [ctypes.c_size_t, _V]),
     "hils_chunk_attn": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V, _V]),
     "hils_fuse": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V]),
     "hils_workspace_init": (ctypes.c_int, [_V, ctypes.c_size_t, _V]),
@@ -474,93 +469,116 @@ def rope(rot_dim, *, layout="half", scaling="plain", base=10000.0, factor=1.0, t
     return r
 
 
-class _On:
-    """The device of `t` made current, and `stream` (default: that device's current stream) made
-    the stream that outputs and workspaces are allocated on; the caller's tensors are kept from
-    reuse until the work given to `stream` is done."""
-
-    def __init__(self, t, stream, used=()):
-        self.guards = ()
-        dev = t.device
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError("stream is on %s, the tensors on %s" % (stream.device, dev))
-            self.guards = (torch.cuda.stream(stream),)
-            for u in used:
-                if u is not None:
-                    u.record_stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self.guards = (torch.cuda.device(dev),)
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        for g in self.guards:
-            g.__exit__(*exc)
+# hils_qk_params and hils_paged_params, packed: these calls are made once per layer and step of a
+# serving loop, where building a ctypes structure field by field would cost as much as the launch
+_QK = struct.Struct("<27q3if")
+_PAGED = struct.Struct("<10q3if")
+assert _QK.size == ctypes.sizeof(QkParams) and _PAGED.size == ctypes.sizeof(PagedParams)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _rows(t, name, dtype, shape, device, out=False):
-    """Checks a tensor whose last dimension is contiguous; the others by any strides (an
-    output's apart from one another)."""
+def _run(device, stream, used, go):
+    """go(stream handle) with `device` current and outputs and workspaces allocated on `stream`
+    (default: the device's current stream); the caller's tensors `used` are kept from reuse until
+    the work given to `stream` is done."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return go(_raw_stream(device.index))
+        with torch.cuda.device(device):
+            return go(_raw_stream(device.index))
+    if stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+    with torch.cuda.stream(stream):
+        for u in used:
+            if u is not None:
+                u.record_stream(stream)
+        return go(stream.cuda_stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()     # (of an empty tensor: 0)
+
+
+def _refuse(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != device or not t.is_cuda:
+    if not t.is_cuda or t.device != device:
         raise ValueError("%s must live on the CUDA device %s (there is no CPU path)" %
                          (name, device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.numel():
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError("the last dimension of %s must be contiguous" % name)
-        if out:
-            # rows apart: from the innermost stride out, each dimension steps past the ones inside
-            span = t.shape[-1]
-            for st, n in sorted((t.stride(i), t.shape[i]) for i in range(t.dim() - 1)
-                                if t.shape[i] > 1):
-                if st < span:
-                    raise ValueError("rows of %s overlap" % name)
-                span = st * n
-    return t
+    raise ValueError("%s must be contiguous in its last dimension" % name)
 
 
-def _str3(t):
-    """Strides of the three outer dimensions of [.., .., .., d] (0 where a dimension is 1)."""
-    return _Strides(*[st if n > 1 else 0 for st, n in zip(t.stride()[:3], t.shape[:3])])
+def _rows(t, name, dtype, shape, device):
+    """Strides of a tensor [..., d] whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or \
+            t.device != device:
+        _refuse(t, name, dtype, shape, device)
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1 and t.numel():
+        _refuse(t, name, dtype, shape, device)
+    return st
+
+
+def _out_rows(t, name, dtype, shape, device):
+    """The same of an output: no two of its rows overlap."""
+    st = _rows(t, name, dtype, shape, device)
+    if not t.is_contiguous() and t.numel():
+        span = shape[-1]
+        for step, n in sorted((a, b) for a, b in zip(st[:-1], shape[:-1]) if b > 1):
+            if step < span:      # (from the innermost stride out: past all the ones inside)
+                raise ValueError("rows of %s overlap" % name)
+            span = step * n
+    return st
+
+
+def _same_strides(a, b, shape):
+    if a != b and any(x != y for x, y, n in zip(a, b, shape) if n > 1):
+        raise ValueError("K and V must have the same strides")
 
 
 def _ints(t, name, shape, device):
-    if t.device != device:
-        raise ValueError("%s must live on %s" % (name, device))
-    return _need(t, name, torch.int32, shape)
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != shape or \
+            t.device != device or not t.is_contiguous():
+        _refuse(t, name, torch.int32, shape, device)
 
 
-def _qk_setup(q, k, w_q, w_k, pos, pos0, eps, norm):
+_NONE = (0, 0, 0, 0)
+
+
+def _qk_setup(q, k, w_q, w_k, pos):
+    """Checks q [B,Hq,N,d], k [B,Hkv,N,d] (either may be None) and what goes with them."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
     if not x.is_cuda:
         raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
     dev, dt = x.device, x.dtype
-    B, _, N, d = x.shape
-    Hq = 0 if q is None else q.shape[1]
-    Hkv = 0 if k is None else k.shape[1]
-    p = QkParams(B=B, N=N, Hq=Hq, Hkv=Hkv, d=d, pos0=pos0, dtype=_dtype_code(dt),
-                 grad_dtype=_dtype_code(dt), norm=int(bool(norm)), eps=eps)
+    B, Hq, N, d = x.shape
+    Hkv = 0
+    sq = sk = _NONE
     if q is not None:
-        p.q_str = _str3(_rows(q, "q", dt, (B, Hq, N, d), dev))
+        sq = _rows(q, "q", dt, (B, Hq, N, d), dev)
+    else:
+        Hq = 0
     if k is not None:
-        p.k_str = _str3(_rows(k, "k", dt, (B, Hkv, N, d), dev))
-    for w, n in ((w_q, "w_q"), (w_k, "w_k")):
-        if w is not None:
-            _rows(w, n, dt, (d,), dev)
+        Hkv = k.shape[1]
+        sk = _rows(k, "k", dt, (B, Hkv, N, d), dev)
+    if w_q is not None:
+        _rows(w_q, "w_q", dt, (d,), dev)
+    if w_k is not None:
+        _rows(w_k, "w_k", dt, (d,), dev)
     if pos is not None:
         _ints(pos, "pos", (B, N), dev)
-    return p, dev, dt
+    return dev, dt, (B, N, Hq, Hkv, d), sq[:3], sk[:3]
+
+
+def _contiguous_like(x, dtype=None):
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rope(q, k, w_q, w_k, rope, *, pos=None, pos0=0, eps=1e-6, norm=True, q_out=None,
@@ -569,20 +587,26 @@ def qk_norm_rope(q, k, w_q, w_k, rope, *, pos=None, pos0=0, eps=1e-6, norm=True,
     k [B,Hkv,N,d] (either may be None) at positions pos [B,N] int32 or pos0 + n.  Any strides over
     a contiguous head dim; outputs default to contiguous tensors, q_out may be q.  norm=False
     only rotates.  Returns (q_out, k_out)."""
-    p, dev, dt = _qk_setup(q, k, w_q, w_k, pos, pos0, eps, norm)
-    with _On(q if q is not None else k, stream, (q, k, w_q, w_k, pos, q_out, k_out)) as st:
+    dev, dt, dims, sq, sk = _qk_setup(q, k, w_q, w_k, pos)
+
+    def go(st):
+        qo = ko = None
+        so = sko = _NONE
         if q is not None:
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=dt, device=dev)
-            p.qo_str = _str3(_rows(q_out, "q_out", dt, q.shape, dev, out=True))
+            qo = _contiguous_like(q) if q_out is None else q_out
+            so = _out_rows(qo, "q_out", dt, q.shape, dev)
         if k is not None:
-            if k_out is None:
-                k_out = torch.empty(k.shape, dtype=dt, device=dev)
-            p.ko_str = _str3(_rows(k_out, "k_out", dt, k.shape, dev, out=True))
-        _check(lib().hils_qk_norm_rope(ctypes.byref(p), ctypes.byref(rope), _ptr(q), _ptr(k),
-                                       _ptr(w_q), _ptr(w_k), _ptr(pos), _ptr(q_out), _ptr(k_out),
-                                       st), "hils_qk_norm_rope")
-    return q_out, k_out
+            ko = _contiguous_like(k) if k_out is None else k_out
+            sko = _out_rows(ko, "k_out", dt, k.shape, dev)
+        code = _dtype_code(dt)
+        p = _QK.pack(*dims, pos0, *sq, *sk, 0, 0, 0, *so[:3], *sko[:3], 0, 0, 0, 0, 0, 0, code,
+                     code, int(bool(norm)), eps)
+        _check(lib().hils_qk_norm_rope(p, ctypes.byref(rope), _addr(q), _addr(k), _addr(w_q),
+                                       _addr(w_k), _addr(pos), _addr(qo), _addr(ko), st),
+               "hils_qk_norm_rope")
+        return qo, ko
+
+    return _run(dev, stream, (q, k, w_q, w_k, pos, q_out, k_out), go)
 
 
 def qk_norm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, rope, *, pos=None, pos0=0, eps=1e-6,
@@ -591,44 +615,39 @@ def qk_norm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, rope, *, pos=None, pos
     outputs (fp32, as backward() returns them, or q's dtype; any strides).  Returns a dict of dq,
     dk (in the gradients' dtype; dq may be dq_out) and dw_q, dw_k (fp32 [d], None where there is
     no weight)."""
-    p, dev, dt = _qk_setup(q, k, w_q, w_k, pos, pos0, eps, norm)
+    dev, dt, dims, sq, sk = _qk_setup(q, k, w_q, w_k, pos)
     gt = (dq_out if q is not None else dk_out).dtype
-    p.grad_dtype = _dtype_code(gt)
-    with _On(q if q is not None else k, stream,
-             (q, k, w_q, w_k, pos, dq_out, dk_out, dq, dk)) as st:
+
+    def go(st):
+        gq = gk = None
+        sgq = sgk = sdq = sdk = _NONE
         if q is not None:
-            p.qo_str = _str3(_rows(dq_out, "dq_out", gt, q.shape, dev))
-            if dq is None:
-                dq = torch.empty(q.shape, dtype=gt, device=dev)
-            p.dq_str = _str3(_rows(dq, "dq", gt, q.shape, dev, out=True))
+            sgq = _rows(dq_out, "dq_out", gt, q.shape, dev)
+            gq = _contiguous_like(q, gt) if dq is None else dq
+            sdq = _out_rows(gq, "dq", gt, q.shape, dev)
         if k is not None:
-            p.ko_str = _str3(_rows(dk_out, "dk_out", gt, k.shape, dev))
-            if dk is None:
-                dk = torch.empty(k.shape, dtype=gt, device=dev)
-            p.dk_str = _str3(_rows(dk, "dk", gt, k.shape, dev, out=True))
-        dw_q, dw_k = [None if w is None else torch.empty(w.shape, dtype=torch.float32, device=dev)
-                      for w in (w_q, w_k)]
-        ws = None
-        if dw_q is not None or dw_k is not None:
-            ws = torch.empty(int(lib().hils_qk_backward_workspace_size(ctypes.byref(p))),
-                             dtype=torch.uint8, device=dev)
+            sgk = _rows(dk_out, "dk_out", gt, k.shape, dev)
+            gk = _contiguous_like(k, gt) if dk is None else dk
+            sdk = _out_rows(gk, "dk", gt, k.shape, dev)
+        p = _QK.pack(*dims, pos0, *sq, *sk, 0, 0, 0, *sgq[:3], *sgk[:3], *sdq[:3], *sdk[:3],
+                     _dtype_code(dt), _dtype_code(gt), int(bool(norm)), eps)
+        dw_q = dw_k = ws = None
+        need = 0
+        if w_q is not None or w_k is not None:
+            need = lib().hils_qk_backward_workspace_size(p)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            if w_q is not None:
+                dw_q = _contiguous_like(w_q, torch.float32)
+            if w_k is not None:
+                dw_k = _contiguous_like(w_k, torch.float32)
         _check(lib().hils_qk_norm_rope_backward(
-            ctypes.byref(p), ctypes.byref(rope), _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k),
-            _ptr(pos), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k),
-            _ptr(ws), 0 if ws is None else ws.numel(), st), "hils_qk_norm_rope_backward")
-    return {"dq": dq, "dk": dk, "dw_q": dw_q, "dw_k": dw_k}
+            p, ctypes.byref(rope), _addr(q), _addr(k), _addr(w_q), _addr(w_k), _addr(pos),
+            _addr(dq_out) if q is not None else None, _addr(dk_out) if k is not None else None,
+            _addr(gq), _addr(gk), _addr(dw_q), _addr(dw_k), _addr(ws), need, st),
+            "hils_qk_norm_rope_backward")
+        return {"dq": gq, "dk": gk, "dw_q": dw_q, "dw_k": dw_k}
 
-
-def _cache_params(K, V, T, B, Hq, max_pages, window=0, scale=0.0):
-    P, Hkv, ps, d = K.shape
-    _rows(K, "K", K.dtype, K.shape, K.device)
-    _rows(V, "V", K.dtype, K.shape, K.device)
-    c = PagedParams(T=T, B=B, Hq=Hq, Hkv=Hkv, d=d, n_pages=P, max_pages=max_pages, page_size=ps,
-                    window=window, dtype=_dtype_code(K.dtype), scale=float(scale))
-    c.c_str = _str3(K)
-    if list(_str3(V)) != list(c.c_str):
-        raise ValueError("K and V must have the same strides")
-    return c
+    return _run(dev, stream, (q, k, w_q, w_k, pos, dq_out, dk_out, dq, dk), go)
 
 
 def paged_workspace(q=None, K=None, *, device=None, stream=None):
@@ -640,10 +659,26 @@ def paged_workspace(q=None, K=None, *, device=None, stream=None):
         c = PagedParams(T=0, B=0, Hq=q.shape[1], Hkv=K.shape[1], d=q.shape[2], page_size=1)
         n = int(lib().hils_paged_workspace_size(ctypes.byref(c)))
         device = q.device
-    buf = torch.empty(n, dtype=torch.uint8, device=device)
-    with _On(buf, stream) as st:
-        _check(lib().hils_workspace_init(_ptr(buf), n, st), "hils_workspace_init")
-    return buf
+    device = torch.device(device)
+    if device.index is None:
+        device = torch.device(device.type, torch.cuda.current_device())
+
+    def go(st):
+        buf = torch.empty(n, dtype=torch.uint8, device=device)
+        _check(lib().hils_workspace_init(_addr(buf), n, st), "hils_workspace_init")
+        return buf
+
+    return _run(device, stream, (), go)
+
+
+def _workspace_of(ws, device, n):
+    """The caller's workspace, or one for this call (its status word zeroed)."""
+    if ws is None:
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+        ws[:256].zero_()
+    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        _refuse(ws, "ws", torch.uint8, ws.shape, device)
+    return ws
 
 
 def paged_plan(kv_len, new_len, block_table, free_pages, n_free, *, page_size, T_cap,
@@ -654,31 +689,37 @@ def paged_plan(kv_len, new_len, block_table, free_pages, n_free, *, page_size, T
     be kv_len and n_free.  Returns a dict: slot, pos, seq [T_cap], cu [B+1], kv_len [B],
     n_free [1], all int32."""
     B, M = block_table.shape
+    P = free_pages.numel()
     dev = block_table.device
-    _need(block_table, "block_table", torch.int32)
+    if not block_table.is_cuda:
+        _refuse(block_table, "block_table", torch.int32, (B, M), dev)
+    _ints(block_table, "block_table", (B, M), dev)
     _ints(kv_len, "kv_len", (B,), dev)
     _ints(new_len, "new_len", (B,), dev)
-    _ints(free_pages, "free_pages", (free_pages.numel(),), dev)
+    _ints(free_pages, "free_pages", (P,), dev)
     _ints(n_free, "n_free", (1,), dev)
-    c = PagedParams(T=T_cap, B=B, n_pages=free_pages.numel(), max_pages=M, page_size=page_size)
-    with _On(block_table, stream, (kv_len, new_len, block_table, free_pages, n_free, kv_len_out,
-                                   n_free_out, ws)) as st:
-        buf = torch.empty((3, max(T_cap, 0)), dtype=torch.int32, device=dev)
-        cu = torch.empty(B + 1, dtype=torch.int32, device=dev)
-        kv_len_out = torch.empty_like(kv_len) if kv_len_out is None else \
-            _ints(kv_len_out, "kv_len_out", (B,), dev)
-        n_free_out = torch.empty_like(n_free) if n_free_out is None else \
-            _ints(n_free_out, "n_free_out", (1,), dev)
-        if ws is None:
-            ws = torch.zeros(256, dtype=torch.uint8, device=dev)
-        slot, pos, seq = buf
-        _check(lib().hils_paged_plan(ctypes.byref(c), _ptr(kv_len), _ptr(new_len),
-                                     _ptr(block_table), _ptr(free_pages), _ptr(n_free),
-                                     _ptr(kv_len_out), _ptr(n_free_out), _ptr(cu), _ptr(slot),
-                                     _ptr(pos), _ptr(seq), _ptr(ws), ws.numel(), st),
-               "hils_paged_plan")
-    return {"slot": slot, "pos": pos, "seq": seq, "cu": cu, "kv_len": kv_len_out,
-            "n_free": n_free_out}
+    if kv_len_out is not None:
+        _ints(kv_len_out, "kv_len_out", (B,), dev)
+    if n_free_out is not None:
+        _ints(n_free_out, "n_free_out", (1,), dev)
+    if T_cap < 0:
+        raise ValueError("T_cap must not be negative")
+
+    def go(st):
+        slot, pos, seq = block_table.new_empty((3, T_cap)).unbind(0)
+        cu = block_table.new_empty(B + 1)
+        kv = torch.empty_like(kv_len) if kv_len_out is None else kv_len_out
+        nf = torch.empty_like(n_free) if n_free_out is None else n_free_out
+        w = _workspace_of(ws, dev, 256)
+        p = _PAGED.pack(T_cap, B, 0, 0, 0, P, M, 0, 0, 0, page_size, 0, 0, 0.0)
+        _check(lib().hils_paged_plan(p, _addr(kv_len), _addr(new_len), _addr(block_table),
+                                     _addr(free_pages), _addr(n_free), _addr(kv), _addr(nf),
+                                     _addr(cu), _addr(slot), _addr(pos), _addr(seq), _addr(w),
+                                     w.numel(), st), "hils_paged_plan")
+        return {"slot": slot, "pos": pos, "seq": seq, "cu": cu, "kv_len": kv, "n_free": nf}
+
+    return _run(dev, stream, (kv_len, new_len, block_table, free_pages, n_free, kv_len_out,
+                              n_free_out, ws), go)
 
 
 def paged_append(q, k, v, w_q, w_k, rope, K, V, pos, slot, *, eps=1e-6, norm=True, q_out=None,
@@ -687,26 +728,39 @@ def paged_append(q, k, v, w_q, w_k, rope, K, V, pos, slot, *, eps=1e-6, norm=Tru
     at pos [T], keys and values written to slot [T] of the pools K, V [n_pages,Hkv,page_size,d]
     (any strides; a [n_pages,page_size,Hkv,d] pool as its transpose).  Returns q_out, whose
     padding rows (slot < 0) are left as they were (zero where it is allocated here)."""
+    if not q.is_cuda:
+        raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
     T, Hq, d = q.shape
     Hkv = k.shape[1]
-    tokens = lambda t: t.transpose(0, 1)[None]     # [T, H, d] as [1, H, T, d]
-    p, dev, dt = _qk_setup(tokens(q), tokens(k), w_q, w_k, None, 0, eps, norm)
-    p.v_str = _str3(tokens(_rows(v, "v", dt, (T, Hkv, d), dev)))
-    _rows(K, "K", dt, (K.shape[0], Hkv, K.shape[2], d), dev, out=True)
-    c = _cache_params(K, V, T, 0, Hq, 0)
+    P, _, ps, _ = K.shape
+    dev, dt = q.device, q.dtype
+    sq = _rows(q, "q", dt, (T, Hq, d), dev)
+    sk = _rows(k, "k", dt, (T, Hkv, d), dev)
+    sv = _rows(v, "v", dt, (T, Hkv, d), dev)
+    for w, n in ((w_q, "w_q"), (w_k, "w_k")):
+        if w is not None:
+            _rows(w, n, dt, (d,), dev)
+    sc = _out_rows(K, "K", dt, (P, Hkv, ps, d), dev)
+    _same_strides(sc, _out_rows(V, "V", dt, (P, Hkv, ps, d), dev), K.shape)
     _ints(pos, "pos", (T,), dev)
     _ints(slot, "slot", (T,), dev)
-    with _On(q, stream, (q, k, v, w_q, w_k, K, V, pos, slot, q_out, ws)) as st:
-        if q_out is None:
-            q_out = torch.zeros((T, Hq, d), dtype=dt, device=dev)
-        p.qo_str = _str3(tokens(_rows(q_out, "q_out", dt, (T, Hq, d), dev, out=True)))
-        if ws is None:
-            ws = torch.zeros(256, dtype=torch.uint8, device=dev)
-        _check(lib().hils_paged_append(ctypes.byref(p), ctypes.byref(rope), ctypes.byref(c),
-                                       _ptr(q), _ptr(k), _ptr(v), _ptr(w_q), _ptr(w_k), _ptr(pos),
-                                       _ptr(slot), _ptr(q_out), _ptr(K), _ptr(V), _ptr(ws),
-                                       ws.numel(), st), "hils_paged_append")
-    return q_out
+
+    def go(st):
+        out = torch.zeros_like(q, memory_format=torch.contiguous_format) if q_out is None \
+            else q_out
+        so = _out_rows(out, "q_out", dt, (T, Hq, d), dev)
+        w = _workspace_of(ws, dev, 256)
+        code = _dtype_code(dt)
+        p = _QK.pack(1, T, Hq, Hkv, d, 0, 0, sq[1], sq[0], 0, sk[1], sk[0], 0, sv[1], sv[0], 0,
+                     so[1], so[0], 0, 0, 0, 0, 0, 0, 0, 0, 0, code, code, int(bool(norm)), eps)
+        c = _PAGED.pack(T, 0, Hq, Hkv, d, P, 0, *sc[:3], ps, 0, code, 0.0)
+        _check(lib().hils_paged_append(p, ctypes.byref(rope), c, _addr(q), _addr(k), _addr(v),
+                                       _addr(w_q), _addr(w_k), _addr(pos), _addr(slot),
+                                       _addr(out), _addr(K), _addr(V), _addr(w), w.numel(), st),
+               "hils_paged_append")
+        return out
+
+    return _run(dev, stream, (q, k, v, w_q, w_k, K, V, pos, slot, q_out, ws), go)
 
 
 def paged_attn(q, K, V, block_table, pos, *, seq=None, window=0, scale=0.0, out=None, lse=None,
@@ -715,35 +769,40 @@ def paged_attn(q, K, V, block_table, pos, *, seq=None, window=0, scale=0.0, out=
     them, if given) of sequence seq[t] (default t) in the pools K, V [n_pages,Hkv,page_size,d]
     (any strides) through block_table [B,max_pages].  Returns (out [T,Hq,d], lse [T,Hq] fp32);
     padding rows (seq < 0) are left as they were (zero where `out` is allocated here)."""
+    if not q.is_cuda:
+        raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
     T, Hq, d = q.shape
-    dt = q.dtype
-    _need(q, "q")
-    dev = q.device
-    _rows(K, "K", dt, K.shape[:3] + (d,), dev)
+    P, Hkv, ps, _ = K.shape
     B, M = block_table.shape
+    dev, dt = q.device, q.dtype
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    sc = _rows(K, "K", dt, (P, Hkv, ps, d), dev)
+    _same_strides(sc, _rows(V, "V", dt, (P, Hkv, ps, d), dev), K.shape)
     _ints(block_table, "block_table", (B, M), dev)
     _ints(pos, "pos", (T,), dev)
     if seq is not None:
         _ints(seq, "seq", (T,), dev)
-    c = _cache_params(K, V, T, B, Hq, M, window, scale)
-    with _On(q, stream, (q, K, V, block_table, pos, seq, out, lse, ws)) as st:
-        new = torch.zeros if seq is not None else torch.empty
-        if out is None:
-            out = new((T, Hq, d), dtype=dt, device=dev)
-        if lse is None:
-            lse = new((T, Hq), dtype=torch.float32, device=dev)
-        if out.device != dev or lse.device != dev:
-            raise ValueError("out and lse must live on %s" % dev)
-        _need(out, "out", dt, (T, Hq, d))
-        _need(lse, "lse", torch.float32, (T, Hq))
-        if ws is None:
-            ws = torch.empty(max(256, int(lib().hils_paged_workspace_size(ctypes.byref(c)))),
-                             dtype=torch.uint8, device=dev)
-            ws[:256].zero_()
-        _check(lib().hils_paged_attn(ctypes.byref(c), _ptr(q), _ptr(K), _ptr(V),
-                                     _ptr(block_table), _ptr(seq), _ptr(pos), _ptr(out),
-                                     _ptr(lse), _ptr(ws), ws.numel(), st), "hils_paged_attn")
-    return out, lse
+    if out is not None and not _need(out, "out", dt, (T, Hq, d)).device == dev:
+        raise ValueError("out must live on %s" % dev)
+    if lse is not None and not _need(lse, "lse", torch.float32, (T, Hq)).device == dev:
+        raise ValueError("lse must live on %s" % dev)
+
+    def go(st):
+        o, z = out, lse
+        if o is None:
+            o = torch.empty_like(q) if seq is None else torch.zeros_like(q)
+        if z is None:
+            z = q.new_empty((T, Hq), dtype=torch.float32) if seq is None else \
+                q.new_zeros((T, Hq), dtype=torch.float32)
+        c = _PAGED.pack(T, B, Hq, Hkv, d, P, M, *sc[:3], ps, window, _dtype_code(dt), scale)
+        w = _workspace_of(ws, dev, 0 if ws is not None else lib().hils_paged_workspace_size(c))
+        _check(lib().hils_paged_attn(c, _addr(q), _addr(K), _addr(V), _addr(block_table),
+                                     _addr(seq), _addr(pos), _addr(o), _addr(z), _addr(w),
+                                     w.numel(), st), "hils_paged_attn")
+        return o, z
+
+    return _run(dev, stream, (q, K, V, block_table, pos, seq, out, lse, ws), go)
 
 
 def version():

@@ -16,16 +16,16 @@ namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
-// Strides (batch, head, token) of a tensor with these sizes: 16-byte multiples, not negative; of
-// an output, rows apart from one another wherever a dimension has more than one entry.
+// Strides of a tensor with these sizes (those of a dimension of one entry are not used): 16-byte
+// multiples, not negative; of an output, at least a row.
 bool ok_strides(const int64_t (&st)[3], int64_t es, int64_t B, int64_t H, int64_t N, int64_t d,
                 bool output) {
   const int64_t n[3] = {B, H, N};
   for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
     if (st[i] < 0 || st[i] % (16 / es) != 0) return false;
-    // (every offset stays within 63 bits of bytes)
-    if (n[i] > 1 && st[i] > (INT64_MAX / 64) / n[i]) return false;
-    if (output && n[i] > 1 && st[i] < d) return false;
+    if (st[i] > (INT64_MAX / 64) / n[i]) return false;   // offsets within 63 bits of bytes
+    if (output && st[i] < d) return false;
   }
   return true;
 }

@@ -89,19 +89,19 @@ __device__ __forceinline__ PaRow pa_row(const PagedAttnArgs& a, int t, bool& bad
   return r;
 }
 
-// Where a stretch of the list begins: the unit (row, head) holds place `begin` and starts at place
-// `unit` (begin >= total, the places of the list: no stretch).
+// Where a stretch of the list begins: row `row`, whose first unit starts at place `at`, holds
+// place `begin` (begin >= total, the places of the list: no stretch).
 struct PaStretch {
-  int64_t begin, total, unit;
-  int row, head;
+  int64_t begin, total, at;
+  int row;
 };
 
-// x / n for 0 <= x < 65536 n: an estimate within one, put right.
+// x / n for 0 <= x < 65536 n: an estimate within one (a reciprocal in fp32), put right.
 __device__ __forceinline__ int pa_head(int64_t x, int n) {
-  int64_t h = (int64_t)__fdividef((float)x, (float)n);
-  while (h * n > x) --h;
-  while ((h + 1) * n <= x) ++h;
-  return (int)h;
+  int h = (int)((double)x * (double)__frcp_rn((float)n));
+  while ((int64_t)h * n > x) --h;
+  while ((int64_t)(h + 1) * n <= x) ++h;
+  return h;
 }
 
 // Places per CTA and per warp, and where the stretches of this CTA's warps begin (in shared memory,
@@ -135,13 +135,10 @@ __device__ __forceinline__ PaPlan pa_schedule(const PagedAttnArgs& a, PaStretch*
     int w = 0;
     while (w < NW && begin + w * P.per_warp < at) ++w;
     for (int t = t0; t < t1 && w < NW; ++t) {
-      const int n = pa_row(a, t, bad).places<KT>();
-      const int64_t next = at + (int64_t)n * a.Hkv;
+      const int64_t next = at + (int64_t)pa_row(a, t, bad).places<KT>() * a.Hkv;
       for (; w < NW && begin + w * P.per_warp < next; ++w) {
-        const int head = pa_head(begin + w * P.per_warp - at, n);
         sS[w].row = t;
-        sS[w].head = head;
-        sS[w].unit = at + (int64_t)head * n;
+        sS[w].at = at;
       }
       at = next;
     }
@@ -218,7 +215,7 @@ struct PaShape {
   }
   static_assert(NW * (ST * STAGE + (GM * D + 4 * GM + SCRATCH) * 4) + 1024 <= 227 * 1024,
                 "fits an SM");
-  static_assert((GM * D + 6 * NW * GM) * 4 <= ST * STAGE, "a part and the join fit a warp's ring");
+  static_assert(GM * D * 4 <= ST * STAGE, "a part fits a warp's ring");
   static_assert(ST >= 3, "two tiles in flight while one is used");
   static_assert(CH == 8 || CH == 16 || CH == 32, "whole rows per copy");
 };
@@ -626,10 +623,11 @@ struct PaWalk {
     end = e;
     step = st;
     turn = tu;
-    unit = s.unit;
     row = s.row;
-    head = s.head;
     R = pa_row(a, row, bad);
+    n = R.template tiles<KT>();
+    head = pa_head(s.begin - s.at, n + 1);
+    unit = s.at + (int64_t)head * (n + 1);
     here(s.begin);
   }
 };
@@ -649,7 +647,6 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   __shared__ uint32_t sMask[NW][ST];
   __shared__ PaStretch sStretch[NW];
   __shared__ PaPart sPart[NW][2];
-  __shared__ uint32_t sMem[2 * NW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.G;
   uint8_t* ring = smem + warp * (ST * S::STAGE);
@@ -658,6 +655,7 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   float* sL = sM + NW * 2 * G;
   float* scratch = sL + NW * 2 * G + warp * S::SCRATCH;
   bool bad = false;
+  cudaTriggerProgrammaticLaunchCompletion();   // the join may be launched (it waits for the end)
   const PaPlan P = pa_schedule<NW, KT>(a, sStretch, bad);
   const PaWs W = pa_carve(a.ws, G, D);
 
@@ -785,74 +783,51 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   if (bad) record_status(a.status, kStatusDeviceCheck);
   __syncthreads();
 
-  // ---- the parts, unit by unit: their members as a bit mask, each one's factor 2^(m - M), and
-  // the unit's maximum M and sum (all behind the last part of the first ring)
-  float* sF = reinterpret_cast<float*>(smem) + G * D;   // [NW][2][G]
-  float* sUM = sF + NW * 2 * G;                         // [NW][2][G], at the unit's first member
-  float* sUL = sUM + NW * 2 * G;
-  for (int x = threadIdx.x; x < 2 * NW * G; x += NT) {
-    const int p = x / G, g = x - p * G;
-    const PaPart f = sPart[p / 2][p % 2];
-    uint32_t mem = 0;
-    int starts = 0, ends = 0;
-    float M = -INFINITY;
-#pragma unroll
-    for (int o = 0; o < 2 * NW; ++o) {
-      const PaPart y = sPart[o / 2][o % 2];
-      if (f.row >= 0 && y.row == f.row && y.head == f.head) {
-        mem |= 1u << o;
-        starts |= y.starts;
-        ends |= y.ends;
-        M = fmaxf(M, sM[o * G + g]);
-      }
-    }
-    if (g == 0) sMem[p] = mem && __ffs(mem) - 1 == p ? mem | (starts && ends ? 1u << 31 : 0u) : 0u;
-    if (mem) {
-      const float base = M == -INFINITY ? 0.f : M;
-      sF[x] = exp2f(sM[x] - base);
-      sUM[x] = M;
-      float L = 0.f;
-#pragma unroll
-      for (int o = 0; o < 2 * NW; ++o)
-        if (mem >> o & 1) L = fmaf(exp2f(sM[o * G + g] - base), sL[o * G + g], L);
-      sUL[x] = L;
-    }
-  }
-  __syncthreads();
-  const uint32_t firsts = __ballot_sync(0xffffffffu, lane < 2 * NW && sMem[lane % (2 * NW)] != 0);
-  constexpr int Q = D / 4;   // a thread adds four dimensions of a head
-  for (uint32_t left = firsts; left; left &= left - 1) {
-    const int p = __ffs(left) - 1;
-    const uint32_t mem = sMem[p];
-    const bool whole = mem >> 31;
-    const PaPart f = sPart[p / 2][p % 2];
+  // ---- the parts, unit by unit.  Lane p of every warp holds part p; a warp adds whole heads
+  static_assert(2 * NW <= 32, "a part per lane");
+  const PaPart f = lane < 2 * NW ? sPart[lane / 2][lane % 2] : PaPart{-1, 0, 0, 0};
+  const uint32_t mem = __match_any_sync(
+      0xffffffffu, f.row < 0 ? ~0ull : ((unsigned long long)f.row << 32 | (uint32_t)f.head));
+  const uint32_t starts = __ballot_sync(0xffffffffu, f.starts);
+  const uint32_t ends = __ballot_sync(0xffffffffu, f.ends);
+  uint32_t firsts = __ballot_sync(0xffffffffu, f.row >= 0 && __ffs(mem) - 1 == lane);
+  constexpr int EPL = D / 32;   // dimensions of a lane
+  for (; firsts; firsts &= firsts - 1) {
+    const int p = __ffs(firsts) - 1;
+    const uint32_t unit = __shfl_sync(0xffffffffu, mem, p);
+    const int row = __shfl_sync(0xffffffffu, f.row, p), head = __shfl_sync(0xffffffffu, f.head, p);
+    const bool whole = (starts & unit) && (ends & unit), in = unit >> lane & 1;
     // the CTA's first unit goes to slot 0, another one that is cut to slot 1
-    const int slot = blockIdx.x * 2 + (f.row == rec.row && f.head == rec.head ? 0 : 1);
-    for (int e = threadIdx.x; e < G * Q; e += NT) {
-      const int g = e / Q, i = 4 * (e % Q);
-      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int slot = blockIdx.x * 2 + (row == rec.row && head == rec.head ? 0 : 1);
+    for (int g = warp; g < G; g += NW) {
+      const float m = in ? sM[lane * G + g] : -INFINITY;
+      const float M = warp_max(m);
+      const float r = in ? exp2f(m - (M == -INFINITY ? 0.f : M)) : 0.f;
+      const float L = warp_sum(in ? r * sL[lane * G + g] : 0.f);
+      float O[EPL];
 #pragma unroll
+      for (int e = 0; e < EPL; ++e) O[e] = 0.f;
+#pragma unroll 4
       for (int o = 0; o < 2 * NW; ++o) {
-        if (!(mem >> o & 1)) continue;
-        const float r = sF[o * G + g];
-        const float4 v = *reinterpret_cast<const float4*>(
-            (o % 2 ? reinterpret_cast<const float*>(smem + (o / 2) * (ST * S::STAGE))
-                   : sO + (o / 2) * G * D) + g * D + i);
-        O.x = fmaf(r, v.x, O.x);
-        O.y = fmaf(r, v.y, O.y);
-        O.z = fmaf(r, v.z, O.z);
-        O.w = fmaf(r, v.w, O.w);
+        const float ro = __shfl_sync(0xffffffffu, r, o);
+        if (!(unit >> o & 1)) continue;
+        const float* v = (o % 2 ? reinterpret_cast<const float*>(smem + (o / 2) * (ST * S::STAGE))
+                                : sO + (o / 2) * G * D) + g * D + lane * EPL;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) O[e] = fmaf(ro, v[e], O[e]);
       }
-      const float L = sUL[p * G + g], M = sUM[p * G + g];
       if (whole) {
-        const int64_t h = (int64_t)f.row * a.Hq + f.head * G + g;
+        const int64_t h = (int64_t)row * a.Hq + head * G + g;
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        float v[4] = {O.x * inv, O.y * inv, O.z * inv, O.w * inv};
-        Elem<T>::store4(static_cast<T*>(a.out) + h * D + i, v);
-        if (a.lse && i == 0) a.lse[h] = pa_lse(M, L);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e)
+          store_out(static_cast<T*>(a.out) + h * D + lane * EPL + e, O[e] * inv);
+        if (a.lse && lane == 0) a.lse[h] = pa_lse(M, L);
       } else {
-        *reinterpret_cast<float4*>(W.o + ((int64_t)slot * G + g) * D + i) = O;
-        if (i == 0)
+#pragma unroll
+        for (int e = 0; e < EPL; ++e)
+          W.o[((int64_t)slot * G + g) * D + lane * EPL + e] = O[e];
+        if (lane == 0)
           *reinterpret_cast<float2*>(W.ml + (slot * G + g) * 2) = make_float2(M, L);
       }
     }
@@ -868,6 +843,7 @@ template <typename T, int D, int NT, bool BY_UNIT>
 __global__ void __launch_bounds__(NT)
     paged_attn_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
   constexpr int NS = NT / D;
+  cudaGridDependencySynchronize();   // launched early: the parts are there from here on
   __shared__ float sF[kPaCtas], sRed[NT / 32], sO[NS][D];
   __shared__ int sC;
   const int g = blockIdx.y, G = a.G;
@@ -968,12 +944,21 @@ cudaError_t launch_both(const PagedAttnArgs& a, cudaStream_t st) {
                    : launch_one<T, D, 16>(b, grid, st);
   if (e != cudaSuccess || grid < 2) return e;
   const int64_t units = (int64_t)a.T * a.Hkv;
-  if (units < grid - 1)
-    paged_attn_join_kernel<T, D, 1024, true>
-        <<<dim3((unsigned)units, a.G), 1024, 0, st>>>(b, grid);
-  else
-    paged_attn_join_kernel<T, D, 256, false><<<dim3(grid - 1, a.G), 256, 0, st>>>(b, grid);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (units < grid - 1) {
+    cfg.gridDim = dim3((unsigned)units, a.G);
+    cfg.blockDim = dim3(1024);
+    return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D, 1024, true>, b, grid);
+  }
+  cfg.gridDim = dim3(grid - 1, a.G);
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D, 256, false>, b, grid);
 }
 
 }  // namespace
