@@ -10,7 +10,7 @@
 // (queries, output) and one per tile.  Every CTA (one per SM, all of its shared memory) takes an
 // equal stretch of the list and every warp an equal stretch of its CTA's, whatever the rows'
 // lengths; CTAs sum the rows' tiles themselves, so nothing about the lengths is needed on the
-// host.  A warp walks its stretch with its own ring of cp.async stages, across unit boundaries,
+// host.  (Short units are not cut; they go with their first place.)  A warp walks its stretch with its own ring of cp.async stages, across unit boundaries,
 // and its own running maximum and sum, and writes units that lie within it: no block barrier
 // until every warp is done.  Then the parts (m, sum, O) of units cut by a warp boundary are added
 // in shared memory, and those of units cut by a CTA boundary go to the workspace, where the join
@@ -31,11 +31,15 @@ namespace {
 
 constexpr int kPaCtas = 148;      // CTAs at most (one per SM of 148)
 constexpr int kPaMinPer = 4;      // places of the list a CTA takes at least
+// Units of up to this many places (and not longer than a warp's stretch) are not cut: joining the
+// parts costs about as much as the tiles that a warp may get too many (2048 units of four tiles:
+// 15.7 us uncut, 20.2 us cut; without this bound ragged rows of up to 1000 tiles lose 20%).
+constexpr int kPaSmall = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // The unit at the start of a CTA's stretch, for the join: the start's place in the unit, the
-// unit's places, and the places per stretch (n = 0: no stretch).
+// unit's places, and the places per stretch (n = 0: no stretch, or a unit that is not cut).
 struct PaRec {
   int64_t off, n, per;
   int32_t row, head;
@@ -96,12 +100,9 @@ struct PaStretch {
   int row;
 };
 
-// x / n for 0 <= x < 65536 n: an estimate within one (a reciprocal in fp32), put right.
+// x / n, in 32 bits where they do.
 __device__ __forceinline__ int pa_head(int64_t x, int n) {
-  int h = (int)((double)x * (double)__frcp_rn((float)n));
-  while ((int64_t)h * n > x) --h;
-  while ((int64_t)(h + 1) * n <= x) ++h;
-  return h;
+  return x < n ? 0 : x < INT32_MAX ? (int)((uint32_t)x / (uint32_t)n) : (int)(x / n);
 }
 
 // Places per CTA and per warp, and where the stretches of this CTA's warps begin (in shared memory,
@@ -575,6 +576,7 @@ struct PaWarp<float, D, GM> {
 template <int KT, int NW>
 struct PaWalk {
   int64_t end, unit;   // end of the stretch, place of the unit
+  int64_t small;       // a unit of up to this many places is not cut: it goes with its first place
   int row, head, n, i0, i1, t0, step, turn;
   bool starts, ends;
   PaRow R;
@@ -584,6 +586,10 @@ struct PaWalk {
     t0 = R.lo / KT;
     i0 = begin > unit ? (int)(begin - unit - 1) : 0;
     i1 = end - unit - 1 < n ? (int)(end - unit - 1) : n;
+    if (n < small) {
+      i0 = begin > unit ? n : 0;
+      i1 = n;
+    }
     starts = i0 == 0;
     ends = i1 == n;
     if (step > 1) {   // the tiles go round the warps; `turn` is this warp's distance to its next
@@ -603,8 +609,15 @@ struct PaWalk {
     }
     here(unit);
   }
-  // the next unit has a tile in the stretch
-  __device__ __forceinline__ bool more() const { return unit + n + 2 < end; }
+  // the next unit begins in the stretch
+  __device__ __forceinline__ bool more() const { return unit + n + 1 < end; }
+  // ends the stretch that begins at `begin` before place e
+  __device__ __forceinline__ void limit(int64_t begin, int64_t e) {
+    if (e < end) {
+      end = e;
+      here(begin);
+    }
+  }
   // to the first unit from here on with a tile for this warp; false if there is none
   __device__ __forceinline__ bool settle(const PagedAttnArgs& a, bool& bad) {
     while (i0 >= i1) {
@@ -619,10 +632,11 @@ struct PaWalk {
     return settle(a, bad);
   }
   __device__ __forceinline__ void open(const PagedAttnArgs& a, const PaStretch& s, int64_t e,
-                                       int st, int tu, bool& bad) {
+                                       int64_t uncut, bool& bad) {
     end = e;
-    step = st;
-    turn = tu;
+    small = uncut;
+    step = 1;
+    turn = 0;
     row = s.row;
     R = pa_row(a, row, bad);
     n = R.template tiles<KT>();
@@ -655,7 +669,6 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   float* sL = sM + NW * 2 * G;
   float* scratch = sL + NW * 2 * G + warp * S::SCRATCH;
   bool bad = false;
-  cudaTriggerProgrammaticLaunchCompletion();   // the join may be launched (it waits for the end)
   const PaPlan P = pa_schedule<NW, KT>(a, sStretch, bad);
   const PaWs W = pa_carve(a.ws, G, D);
 
@@ -669,26 +682,30 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   bool round = false;
   const int64_t total = sStretch[0].total;
   const int64_t cta_end = sStretch[0].begin + P.per < total ? sStretch[0].begin + P.per : total;
+  const int64_t uncut = P.per_warp < kPaSmall ? P.per_warp : kPaSmall;
   PaRec rec = {};
   rec.per = P.per;
   if (more) {
-    w.open(a, sStretch[0], cta_end, 1, 0, bad);
+    w.open(a, sStretch[0], cta_end, uncut, bad);
     rec.off = sStretch[0].begin - w.unit;
-    rec.n = w.n + 1;
+    rec.n = w.n < w.small ? 0 : w.n + 1;
     rec.row = w.row;
     rec.head = w.head;
-    if (w.more()) w.next_unit(a, bad);
-    round = !w.more();
+    PaWalk<KT, NW> next = w;
+    if (next.more()) next.next_unit(a, bad);
+    round = !next.more();
+    if (round) {
+      w.step = NW;
+      w.turn = warp;
+      w.here(sStretch[0].begin);
+    } else if (warp > 0) {
+      more = sStretch[warp].begin < cta_end;
+      if (more) w.open(a, sStretch[warp], cta_end, uncut, bad);
+    }
+    if (!round && more) w.limit(sStretch[warp].begin, sStretch[warp].begin + P.per_warp);
+    if (more) more = w.settle(a, bad);
   }
   if (threadIdx.x == 0) W.rec[blockIdx.x] = rec;
-  const PaStretch& mine = sStretch[round ? 0 : warp];
-  more = mine.begin < cta_end;
-  const int64_t my_end =
-      round || mine.begin + P.per_warp > cta_end ? cta_end : mine.begin + P.per_warp;
-  if (more) {
-    w.open(a, mine, my_end, round ? NW : 1, warp, bad);
-    more = w.settle(a, bad);
-  }
   PaWalk<KT, NW> u = w;   // the same walk, for the products
   bool go = more;
   int page = -1;
@@ -790,46 +807,45 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
       0xffffffffu, f.row < 0 ? ~0ull : ((unsigned long long)f.row << 32 | (uint32_t)f.head));
   const uint32_t starts = __ballot_sync(0xffffffffu, f.starts);
   const uint32_t ends = __ballot_sync(0xffffffffu, f.ends);
-  uint32_t firsts = __ballot_sync(0xffffffffu, f.row >= 0 && __ffs(mem) - 1 == lane);
+  const uint32_t firsts = __ballot_sync(0xffffffffu, f.row >= 0 && __ffs(mem) - 1 == lane);
   constexpr int EPL = D / 32;   // dimensions of a lane
-  for (; firsts; firsts &= firsts - 1) {
-    const int p = __ffs(firsts) - 1;
+  const int pairs = __popc(firsts) * G;
+  for (int x = warp; x < pairs; x += NW) {
+    const int g = x % G;
+    uint32_t left = firsts;
+    for (int k = x / G; k > 0; --k) left &= left - 1;
+    const int p = __ffs(left) - 1;
     const uint32_t unit = __shfl_sync(0xffffffffu, mem, p);
     const int row = __shfl_sync(0xffffffffu, f.row, p), head = __shfl_sync(0xffffffffu, f.head, p);
     const bool whole = (starts & unit) && (ends & unit), in = unit >> lane & 1;
     // the CTA's first unit goes to slot 0, another one that is cut to slot 1
     const int slot = blockIdx.x * 2 + (row == rec.row && head == rec.head ? 0 : 1);
-    for (int g = warp; g < G; g += NW) {
-      const float m = in ? sM[lane * G + g] : -INFINITY;
-      const float M = warp_max(m);
-      const float r = in ? exp2f(m - (M == -INFINITY ? 0.f : M)) : 0.f;
-      const float L = warp_sum(in ? r * sL[lane * G + g] : 0.f);
-      float O[EPL];
+    const float m = in ? sM[lane * G + g] : -INFINITY;
+    const float M = warp_max(m);
+    const float r = in ? exp2f(m - (M == -INFINITY ? 0.f : M)) : 0.f;
+    const float L = warp_sum(in ? r * sL[lane * G + g] : 0.f);
+    float O[EPL];
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) O[e] = 0.f;
-#pragma unroll 4
-      for (int o = 0; o < 2 * NW; ++o) {
-        const float ro = __shfl_sync(0xffffffffu, r, o);
-        if (!(unit >> o & 1)) continue;
-        const float* v = (o % 2 ? reinterpret_cast<const float*>(smem + (o / 2) * (ST * S::STAGE))
-                                : sO + (o / 2) * G * D) + g * D + lane * EPL;
+    for (int e = 0; e < EPL; ++e) O[e] = 0.f;
+    for (uint32_t of = unit; of; of &= of - 1) {
+      const int o = __ffs(of) - 1;
+      const float ro = __shfl_sync(0xffffffffu, r, o);
+      const float* v = (o % 2 ? reinterpret_cast<const float*>(smem + (o / 2) * (ST * S::STAGE))
+                              : sO + (o / 2) * G * D) + g * D + lane * EPL;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) O[e] = fmaf(ro, v[e], O[e]);
-      }
-      if (whole) {
-        const int64_t h = (int64_t)row * a.Hq + head * G + g;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+      for (int e = 0; e < EPL; ++e) O[e] = fmaf(ro, v[e], O[e]);
+    }
+    if (whole) {
+      const int64_t h = (int64_t)row * a.Hq + head * G + g;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e)
-          store_out(static_cast<T*>(a.out) + h * D + lane * EPL + e, O[e] * inv);
-        if (a.lse && lane == 0) a.lse[h] = pa_lse(M, L);
-      } else {
+      for (int e = 0; e < EPL; ++e)
+        store_out(static_cast<T*>(a.out) + h * D + lane * EPL + e, O[e] * inv);
+      if (a.lse && lane == 0) a.lse[h] = pa_lse(M, L);
+    } else {
 #pragma unroll
-        for (int e = 0; e < EPL; ++e)
-          W.o[((int64_t)slot * G + g) * D + lane * EPL + e] = O[e];
-        if (lane == 0)
-          *reinterpret_cast<float2*>(W.ml + (slot * G + g) * 2) = make_float2(M, L);
-      }
+      for (int e = 0; e < EPL; ++e) W.o[((int64_t)slot * G + g) * D + lane * EPL + e] = O[e];
+      if (lane == 0) *reinterpret_cast<float2*>(W.ml + (slot * G + g) * 2) = make_float2(M, L);
     }
   }
 }
@@ -843,7 +859,6 @@ template <typename T, int D, int NT, bool BY_UNIT>
 __global__ void __launch_bounds__(NT)
     paged_attn_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
   constexpr int NS = NT / D;
-  cudaGridDependencySynchronize();   // launched early: the parts are there from here on
   __shared__ float sF[kPaCtas], sRed[NT / 32], sO[NS][D];
   __shared__ int sC;
   const int g = blockIdx.y, G = a.G;
@@ -944,21 +959,14 @@ cudaError_t launch_both(const PagedAttnArgs& a, cudaStream_t st) {
                    : launch_one<T, D, 16>(b, grid, st);
   if (e != cudaSuccess || grid < 2) return e;
   const int64_t units = (int64_t)a.T * a.Hkv;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (units < grid - 1) {
-    cfg.gridDim = dim3((unsigned)units, a.G);
-    cfg.blockDim = dim3(1024);
-    return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D, 1024, true>, b, grid);
-  }
-  cfg.gridDim = dim3(grid - 1, a.G);
-  cfg.blockDim = dim3(256);
-  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<T, D, 256, false>, b, grid);
+  // (launched early by programmatic dependent launch the join gained nothing: one row of 1000
+  // tokens 11.0 us against 10.2 us)
+  if (units < grid - 1)
+    paged_attn_join_kernel<T, D, 1024, true>
+        <<<dim3((unsigned)units, a.G), 1024, 0, st>>>(b, grid);
+  else
+    paged_attn_join_kernel<T, D, 256, false><<<dim3(grid - 1, a.G), 256, 0, st>>>(b, grid);
+  return cudaGetLastError();
 }
 
 }  // namespace
