@@ -59,6 +59,16 @@ void copy3(int64_t (&to)[3], const int64_t (&from)[3]) {
   for (int i = 0; i < 3; ++i) to[i] = from[i];
 }
 
+// freq / (2 pi) mod 1 in units of 2^-64: positions are whole, so position times this, modulo 2^64, is
+// the angle modulo one turn (within position 2^-65 turns and the rounding of the quotient to 64
+// bits), and no floating-point reduction is needed on the device.
+uint64_t turn_fraction(double freq) {
+  const long double t = (long double)freq / 6.283185307179586476925286766559005768L;
+  const long double f = t - floorl(t);                        // [0, 1]
+  const long double u = floorl(f * 18446744073709551616.0L + 0.5L);
+  return u >= 18446744073709551616.0L ? 0 : (uint64_t)u;      // (a whole turn is none)
+}
+
 QkArgs qk_args(const hils_qk_params* p, const hils_rope* rope) {
   QkArgs a = {};
   a.N = p->N;
@@ -75,7 +85,7 @@ QkArgs qk_args(const hils_qk_params* p, const hils_rope* rope) {
   a.rope.rot = rope->rot_dim;
   a.rope.interleaved = rope->layout == HILS_ROPE_INTERLEAVED;
   a.rope.mscale = rope->mscale;
-  for (int m = 0; m < rope->rot_dim / 2; ++m) a.rope.turn[m] = rope->freq[m] / kTwoPi;
+  for (int m = 0; m < rope->rot_dim / 2; ++m) a.rope.turn[m] = turn_fraction(rope->freq[m]);
   return a;
 }
 

@@ -11,8 +11,9 @@
 // Bound: HBM (a row is read once and written once, about ten flops an element).
 // Layout: eight elements per lane (16 bytes of bf16), LPR lanes per row (8, 16 or 32 by the head
 // dim), so a warp reads whole rows in one or two wide loads.  A lane group keeps one token and
-// walks its heads: its eight cosines and sines are computed once (fp64 turns, reduced to a
-// quarter turn, so far positions lose nothing) and serve every head.  In the half layout the
+// walks its heads: its eight cosines and sines are computed once and serve every head.  The angle
+// is position times a 64-bit fraction of a turn, modulo 2^64: exact, so far positions lose
+// nothing, and two integer products where fp64 arithmetic took a fifth of the kernel's time.  In the half layout the
 // partner of a lane's eight elements is another lane's eight (rot is a multiple of 16), one
 // shuffle per word; in the interleaved layout it is in the lane.
 #include <type_traits>
@@ -24,7 +25,10 @@ namespace hils {
 namespace {
 
 constexpr int kQkThreads = 256;
-constexpr int kQkRows = 4;   // heads of a lane group in flight together (forward)
+constexpr int kQkBlocks = 3;   // blocks per SM (forward)
+// heads of a lane group loaded together (forward); as many more are on their way
+template <typename T>
+constexpr int kQkRows = sizeof(T) == 2 ? 4 : 2;
 
 // Eight elements of a row as the words they are stored in.
 template <typename T>
@@ -35,10 +39,11 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = 0u;
   }
+  // (read once: streaming loads leave the cache to the outputs)
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
     for (int i = 0; i < W / 4; ++i) {
-      const uint4 t = reinterpret_cast<const uint4*>(p)[i];
+      const uint4 t = __ldcs(reinterpret_cast<const uint4*>(p) + i);
       w[4 * i] = t.x; w[4 * i + 1] = t.y; w[4 * i + 2] = t.z; w[4 * i + 3] = t.w;
     }
   }
@@ -94,20 +99,25 @@ struct LaneTurn {
   bool on;       // this lane's elements turn
   bool cross;    // the partners are another lane's (uniform over the warp)
 
-  __device__ __forceinline__ void pair(const RopeTable& R, double pos, int m, float& co,
+  // cosine and sine of pair m at the position: the nearest quarter turn, and the Taylor polynomials
+  // of the rest (at most an eighth turn, where their next terms are below 2^-28)
+  __device__ __forceinline__ void pair(const RopeTable& R, int64_t pos, int m, float& co,
                                        float& si) const {
-    const double quarters = 4.0 * (pos * R.turn[m]);
-    const double k = rint(quarters);
-    float sn, cs;
-    sincospif(0.5f * (float)(quarters - k), &sn, &cs);   // at most an eighth turn
-    switch ((int)((long long)k & 3)) {
-      case 0: co = cs; si = sn; break;
-      case 1: co = -sn; si = cs; break;
-      case 2: co = -cs; si = -sn; break;
-      default: co = sn; si = -cs; break;
-    }
-    co *= R.mscale;
-    si *= R.mscale;
+    const uint64_t turns = (uint64_t)pos * R.turn[m];
+    const uint32_t hi = (uint32_t)(turns >> 32), quarter = (hi + 0x20000000u) >> 30;
+    const int64_t rest = (int64_t)(turns - ((uint64_t)quarter << 62));   // below 2^61
+    const float x = (float)(int32_t)(rest >> 30) * (6.2831853071795865f / 17179869184.f);
+    const float z = x * x;
+    const float sn =
+        x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), 1.f);
+    const float cs = fmaf(
+        z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24),
+                -0.5f), 1.f);
+    // quarters 1 and 3 exchange the two, 1 and 2 negate the cosine, 2 and 3 the sine
+    co = R.mscale * ((quarter & 1) ? sn : cs);
+    si = R.mscale * ((quarter & 1) ? cs : sn);
+    if ((quarter + 1) & 2) co = -co;
+    if (quarter & 2) si = -si;
   }
   __device__ __forceinline__ void init(const RopeTable& R, int p, bool live, int64_t position) {
     const int half = R.rot / 2;
@@ -117,7 +127,7 @@ struct LaneTurn {
 #pragma unroll
     for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
     if (!on || !live) return;
-    const double pos = (double)position;
+    const int64_t pos = position;
     if (cross) {
       const int m0 = 8 * p < half ? 8 * p : 8 * p - half;
       const float sign = 8 * p < half ? -1.f : 1.f;
@@ -155,11 +165,24 @@ __device__ __forceinline__ int64_t token_offset(const QkArgs& a, const int64_t (
   return b * st[0] + (t - b * a.N) * st[2];
 }
 
-// Norm and rotation of rows h0, h0 + hs, ... < H of one token: src + h sh -> dst + h dh.
+// Rows h0 + (i0 + u) hs, u < kQkRows<T>, of one token's H rows (zeros past the end).
+template <typename T>
+__device__ __forceinline__ void load_rows(Raw8<T> (&x)[kQkRows<T>], bool act, const T* src,
+                                          int64_t sh, int H, int h0, int hs, int i0) {
+#pragma unroll
+  for (int u = 0; u < kQkRows<T>; ++u) {
+    const int h = (i0 + u) * hs + h0;
+    x[u].zero();
+    if (act && h < H) x[u].load(src + h * sh);
+  }
+}
+
+// Norm and rotation of rows h0, h0 + hs, ... < H of one token: src + h sh -> dst + h dh.  `x` holds
+// the first rows; the rows after next are on their way while the present ones are turned.
 template <typename T, int LPR>
 __device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, int p, bool act,
-                                          const T* src, int64_t sh, T* dst, int64_t dh, int H,
-                                          int h0, int hs, const void* w) {
+                                          Raw8<T> (&x)[kQkRows<T>], const T* src, int64_t sh, T* dst,
+                                          int64_t dh, int H, int h0, int hs, const void* w) {
   float cw[8], sw[8];
   {
     float own[8], other[8];
@@ -172,17 +195,12 @@ __device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, in
     }
   }
   const float inv_d = 1.f / (float)a.d;
-  for (int hb = 0; hb < H; hb += hs * kQkRows) {
-    Raw8<T> x[kQkRows];
+  for (int i0 = 0; i0 * hs < H; i0 += kQkRows<T>) {
+    Raw8<T> ahead[kQkRows<T>];
+    load_rows<T>(ahead, act, src, sh, H, h0, hs, i0 + kQkRows<T>);
 #pragma unroll
-    for (int u = 0; u < kQkRows; ++u) {
-      const int h = hb + u * hs + h0;
-      x[u].zero();
-      if (act && h < H) x[u].load(src + h * sh);
-    }
-#pragma unroll
-    for (int u = 0; u < kQkRows; ++u) {
-      const int h = hb + u * hs + h0;
+    for (int u = 0; u < kQkRows<T>; ++u) {
+      const int h = (i0 + u) * hs + h0;
       float v[8], o[8];
       x[u].get(v);
       float r = 1.f;
@@ -207,6 +225,7 @@ __device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, in
         x[u].put(v);
         x[u].store(dst + h * dh);
       }
+      x[u] = ahead[u];
     }
   }
 }
@@ -214,7 +233,7 @@ __device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, in
 // grid: blocks of 2^tbl tokens; a lane group holds token (group mod 2^tbl) and the heads
 // (group / 2^tbl) mod the groups per token.
 template <typename T, int LPR, bool PAGED>
-__global__ void __launch_bounds__(kQkThreads)
+__global__ void __launch_bounds__(kQkThreads, kQkBlocks)
     qk_norm_rope_kernel(const __grid_constant__ QkArgs a, int tbl) {
   constexpr int NLG = kQkThreads / LPR;
   const int lg = threadIdx.x / LPR, p = threadIdx.x % LPR;
@@ -233,33 +252,37 @@ __global__ void __launch_bounds__(kQkThreads)
   const bool act = live && 8 * p < a.d;
   int64_t position = 0;
   if (live) position = a.pos ? (int64_t)a.pos[t] : a.pos0 + t % a.N;
+  const int64_t tt = live ? t : 0;
+  const T* q = static_cast<const T*>(a.q) + token_offset(a, a.qs, tt) + 8 * p;
+  const T* k = static_cast<const T*>(a.k) + token_offset(a, a.ks, tt) + 8 * p;
+  Raw8<T> x[kQkRows<T>];
+  load_rows<T>(x, act, q, a.qs[1], a.Hq, h0, hs, 0);
   LaneTurn L;
   L.init(a.rope, p, live, position);
-  const int64_t tt = live ? t : 0;
-  if (a.Hq > 0)
-    turn_rows<T, LPR>(a, L, p, act, static_cast<const T*>(a.q) + token_offset(a, a.qs, tt) + 8 * p,
-                      a.qs[1], static_cast<T*>(a.qo) + token_offset(a, a.qos, tt) + 8 * p,
-                      a.qos[1], a.Hq, h0, hs, a.wq);
-  if (a.Hkv > 0) {
-    const T* k = static_cast<const T*>(a.k) + token_offset(a, a.ks, tt) + 8 * p;
-    if constexpr (PAGED) {
-      const int64_t page = slot < 0 ? 0 : slot / a.page_size;
-      const int64_t off = page * a.cs[0] + (live ? slot - page * a.page_size : 0) * a.cs[2] + 8 * p;
-      turn_rows<T, LPR>(a, L, p, act, k, a.ks[1], static_cast<T*>(a.Kc) + off, a.cs[1], a.Hkv, h0,
-                        hs, a.wk);
-      if (act) {
-        const T* v = static_cast<const T*>(a.v) + token_offset(a, a.vs, tt) + 8 * p;
-        for (int h = h0; h < a.Hkv; h += hs) {
-          Raw8<T> x;
-          x.load(v + h * a.vs[1]);
-          x.store(static_cast<T*>(a.Vc) + off + h * a.cs[1]);
-        }
+  turn_rows<T, LPR>(a, L, p, act, x, q, a.qs[1],
+                    static_cast<T*>(a.qo) + token_offset(a, a.qos, tt) + 8 * p, a.qos[1], a.Hq,
+                    h0, hs, a.wq);
+  load_rows<T>(x, act, k, a.ks[1], a.Hkv, h0, hs, 0);
+  if constexpr (PAGED) {
+    const int64_t page = live ? slot / a.page_size : 0;
+    const int64_t off = page * a.cs[0] + (live ? slot - page * a.page_size : 0) * a.cs[2] + 8 * p;
+    Raw8<T> y[kQkRows<T>];
+    const T* v = static_cast<const T*>(a.v) + token_offset(a, a.vs, tt) + 8 * p;
+    load_rows<T>(y, act, v, a.vs[1], a.Hkv, h0, hs, 0);
+    turn_rows<T, LPR>(a, L, p, act, x, k, a.ks[1], static_cast<T*>(a.Kc) + off, a.cs[1], a.Hkv,
+                      h0, hs, a.wk);
+    for (int i0 = 0; i0 * hs < a.Hkv; i0 += kQkRows<T>) {
+      if (i0 > 0) load_rows<T>(y, act, v, a.vs[1], a.Hkv, h0, hs, i0);
+#pragma unroll
+      for (int u = 0; u < kQkRows<T>; ++u) {
+        const int h = (i0 + u) * hs + h0;
+        if (act && h < a.Hkv) y[u].store(static_cast<T*>(a.Vc) + off + h * a.cs[1]);
       }
-    } else {
-      turn_rows<T, LPR>(a, L, p, act, k, a.ks[1],
-                        static_cast<T*>(a.ko) + token_offset(a, a.kos, tt) + 8 * p, a.kos[1],
-                        a.Hkv, h0, hs, a.wk);
     }
+  } else {
+    turn_rows<T, LPR>(a, L, p, act, x, k, a.ks[1],
+                      static_cast<T*>(a.ko) + token_offset(a, a.kos, tt) + 8 * p, a.kos[1], a.Hkv,
+                      h0, hs, a.wk);
   }
 }
 

@@ -15,7 +15,7 @@ constexpr int kQkBwdBlocks = 592;
 struct RopeTable {
   int32_t rot, interleaved;
   float mscale;
-  double turn[kQkMaxPairs];   // turns per position of pair m: freq / (2 pi)
+  uint64_t turn[kQkMaxPairs];   // pair m's turns per position, freq / (2 pi) mod 1, times 2^64
 };
 
 // Row addressing: element (b, h, n, i) of a tensor at base + b st[0] + h st[1] + n st[2] + i.
