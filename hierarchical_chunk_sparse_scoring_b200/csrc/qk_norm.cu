@@ -8,14 +8,18 @@
 // Backward: g = R_p^T dy (the same with s negated), dw = sum g x r,
 // dx = r (w g - x r^2 mean(w g x)).
 //
-// Bound: HBM (a row is read once and written once, about ten flops an element).
-// Layout: eight elements per lane (16 bytes of bf16), LPR lanes per row (8, 16 or 32 by the head
-// dim), so a warp reads whole rows in one or two wide loads.  A lane group keeps one token and
-// walks its heads: its eight cosines and sines are computed once and serve every head.  The angle
-// is position times a 64-bit fraction of a turn, modulo 2^64: exact, so far positions lose
-// nothing, and two integer products where fp64 arithmetic took a fifth of the kernel's time.  In the half layout the
-// partner of a lane's eight elements is another lane's eight (rot is a multiple of 16), one
-// shuffle per word; in the interleaved layout it is in the lane.
+// Bound: HBM, and close behind it instruction issue: a row of 128 bf16 is read and written once
+// (512 bytes, 12 ns of one SM's share of HBM), so that about 140 instructions for a warp's step of
+// two rows already take as long as the copies (125 us for 32768 tokens of 40 heads, floor 104 us).
+// Hence:
+//   - a lane holds eight elements as two pieces of four, which in the half layout are both members
+//     of four pairs (dims 4p .. and rot/2 + 4p ..): a rotation never leaves its lane, and the only
+//     exchange is the sum of squares over the row's LPR lanes (8, 16 or 32 by the head dim);
+//   - products and sums go two at a time (f32x2);
+//   - a lane group keeps one token and walks its heads: the token's four cosines and sines per
+//     lane are computed once.  The angle is position times a 64-bit fraction of a turn, modulo
+//     2^64: exact, so far positions lose nothing, and two integer products;
+//   - the next heads' rows are loaded while the present ones are turned.
 #include <type_traits>
 
 #include "common.cuh"
@@ -25,62 +29,92 @@ namespace hils {
 namespace {
 
 constexpr int kQkThreads = 256;
-constexpr int kQkBlocks = 3;   // blocks per SM (forward)
+constexpr int kQkBlocks = 3;    // blocks per SM (forward)
+constexpr int kBwdBlocks = 2;
+constexpr int kBwdRows = 2;     // heads of a lane group loaded together (backward)
 // heads of a lane group loaded together (forward); as many more are on their way
 template <typename T>
 constexpr int kQkRows = sizeof(T) == 2 ? 4 : 2;
 
-// Eight elements of a row as the words they are stored in.
+// ---- two fp32 numbers in one register pair
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A lane's eight elements as they are stored: pieces of four at element offsets e0 and e1.
 template <typename T>
 struct Raw8 {
-  static constexpr int W = sizeof(T) * 8 / 4;
-  uint32_t w[W];
+  static constexpr int W = sizeof(T);   // words per piece: 2 (bf16) or 4
+  uint32_t w[2][W];
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = 0u;
+    for (int i = 0; i < W; ++i) w[0][i] = w[1][i] = 0u;
   }
   // (read once: streaming loads leave the cache to the outputs)
-  __device__ __forceinline__ void load(const T* p) {
+  __device__ __forceinline__ void load(const T* row, int e0, int e1) {
 #pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const uint4 t = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-      w[4 * i] = t.x; w[4 * i + 1] = t.y; w[4 * i + 2] = t.z; w[4 * i + 3] = t.w;
-    }
-  }
-  __device__ __forceinline__ void store(T* p) const {
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i)
-      reinterpret_cast<uint4*>(p)[i] =
-          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(w[i]); v[2 * i + 1] = bf16_hi(w[i]); }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-    }
-  }
-  __device__ __forceinline__ void put(const float (&v)[8]) {
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int h = 0; h < 2; ++h) {
+      const T* p = row + (h ? e1 : e0);
+      if constexpr (sizeof(T) == 2) {
+        const uint2 t = __ldcs(reinterpret_cast<const uint2*>(p));
+        w[h][0] = t.x; w[h][1] = t.y;
+      } else {
+        const uint4 t = __ldcs(reinterpret_cast<const uint4*>(p));
+        w[h][0] = t.x; w[h][1] = t.y; w[h][2] = t.z; w[h][3] = t.w;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
     }
   }
-  // the same words of lane `src` of the lane group
-  template <int LPR>
-  __device__ __forceinline__ Raw8 from_lane(int src) const {
-    Raw8 r;
+  __device__ __forceinline__ void store(T* row, int e0, int e1) const {
 #pragma unroll
-    for (int i = 0; i < W; ++i) r.w[i] = __shfl_sync(0xffffffffu, w[i], src, LPR);
-    return r;
+    for (int h = 0; h < 2; ++h) {
+      T* p = row + (h ? e1 : e0);
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[h][0], w[h][1]);
+      else
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
+    }
+  }
+  // v[0], v[1]: the first piece; v[2], v[3]: the second
+  __device__ __forceinline__ void get(f2 (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2)
+        v[i] = pack2(bf16_lo(w[i / 2][i % 2]), bf16_hi(w[i / 2][i % 2]));
+      else
+        v[i] = pack2(__uint_as_float(w[i / 2][2 * (i % 2)]),
+                     __uint_as_float(w[i / 2][2 * (i % 2) + 1]));
+    }
+  }
+  __device__ __forceinline__ void put(const f2 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = unpack2(v[i]);
+      if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(t.x, t.y);
+        w[i / 2][i % 2] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[i / 2][2 * (i % 2)] = __float_as_uint(t.x);
+        w[i / 2][2 * (i % 2) + 1] = __float_as_uint(t.y);
+      }
+    }
   }
 };
 
@@ -91,14 +125,45 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// What a lane needs to turn its eight elements 8p .. 8p + 7 of a head at one position: cosine
-// and signed sine per element (element i becomes x_i c_i + x_partner s_i).
-struct LaneTurn {
-  float c[8], s[8];
-  int partner;   // lane of the group that holds the partners (half layout; else this lane)
-  bool on;       // this lane's elements turn
-  bool cross;    // the partners are another lane's (uniform over the warp)
+// ... of the products a_i b_i of every lane's eight elements
+template <int LPR>
+__device__ __forceinline__ float group_dot(const f2 (&a)[4], const f2 (&b)[4]) {
+  f2 s = mul2(a[0], b[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(a[i], b[i], s);
+  const float2 t = unpack2(s);
+  return group_sum<LPR>(t.x + t.y);
+}
 
+// The partners of a lane's elements, in the same order.
+__device__ __forceinline__ void partners(const f2 (&v)[4], bool interleaved, f2 (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (interleaved) {
+      const float2 t = unpack2(v[i]);
+      o[i] = pack2(t.y, t.x);
+    } else {
+      o[i] = v[i ^ 2];
+    }
+  }
+}
+
+// What a lane needs to turn its eight elements at one position: where they are, and cosine and
+// signed sine per element (element i becomes x_i c_i + x_partner s_i).
+struct LaneTurn {
+  int e0, e1;     // first elements of its pieces
+  bool on;        // they turn
+  f2 c[4], s[4];
+
+  __device__ __forceinline__ void place(const RopeTable& R, int p) {
+    on = 8 * p < R.rot;
+    e0 = 8 * p;
+    e1 = 8 * p + 4;
+    if (on && !R.interleaved) {
+      e0 = 4 * p;
+      e1 = R.rot / 2 + 4 * p;
+    }
+  }
   // cosine and sine of pair m at the position: the nearest quarter turn, and the Taylor polynomials
   // of the rest (at most an eighth turn, where their next terms are below 2^-28)
   __device__ __forceinline__ void pair(const RopeTable& R, int64_t pos, int m, float& co,
@@ -119,111 +184,107 @@ struct LaneTurn {
     if ((quarter + 1) & 2) co = -co;
     if (quarter & 2) si = -si;
   }
-  __device__ __forceinline__ void init(const RopeTable& R, int p, bool live, int64_t position) {
-    const int half = R.rot / 2;
-    on = 8 * p < R.rot;
-    cross = !R.interleaved;
-    partner = !cross || !on ? p : (8 * p < half ? p + half / 8 : p - half / 8);
+  __device__ __forceinline__ void turn_to(const RopeTable& R, int64_t pos) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
-    if (!on || !live) return;
-    const int64_t pos = position;
-    if (cross) {
-      const int m0 = 8 * p < half ? 8 * p : 8 * p - half;
-      const float sign = 8 * p < half ? -1.f : 1.f;
+    for (int i = 0; i < 4; ++i) { c[i] = pack2(1.f, 1.f); s[i] = 0ull; }
+    if (!on) return;
+    float co[4], si[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        pair(R, pos, m0 + i, c[i], s[i]);
-        s[i] *= sign;
-      }
-    } else {
+    for (int i = 0; i < 4; ++i) pair(R, pos, (R.interleaved ? e0 / 2 : e0) + i, co[i], si[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pair(R, pos, 4 * p + i, c[2 * i], s[2 * i + 1]);
-        c[2 * i + 1] = c[2 * i];
-        s[2 * i] = -s[2 * i + 1];
+    for (int i = 0; i < 4; ++i) {
+      if (R.interleaved) {
+        c[i] = pack2(co[i], co[i]);
+        s[i] = pack2(-si[i], si[i]);
+      } else {
+        const int j = 2 * (i & 1);
+        c[i] = pack2(co[j], co[j + 1]);
+        s[i] = i < 2 ? pack2(-si[j], -si[j + 1]) : pack2(si[j], si[j + 1]);
       }
     }
   }
 };
 
-// This lane's eight norm weights and those of its partners (ones without a weight vector).
+// This lane's eight norm weights (ones without a weight vector).
 template <typename T>
-__device__ __forceinline__ void load_weights(const void* w, int e0, int d, float (&v)[8]) {
+__device__ __forceinline__ void load_weights(const void* w, const LaneTurn& L, bool in_row,
+                                             f2 (&v)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 1.f;
-  if (w && e0 < d) {
+  for (int i = 0; i < 4; ++i) v[i] = pack2(1.f, 1.f);
+  if (w && in_row) {
     Raw8<T> r;
-    r.load(static_cast<const T*>(w) + e0);
+    r.load(static_cast<const T*>(w), L.e0, L.e1);
     r.get(v);
   }
 }
 
+// Offset of token t (fewer than 2^31) by strides (batch, head, token).
 __device__ __forceinline__ int64_t token_offset(const QkArgs& a, const int64_t (&st)[3],
                                                 int64_t t) {
-  const int64_t b = t / a.N;
+  if (t < a.N) return t * st[2];
+  const uint32_t b = (uint32_t)t / (uint32_t)a.N;
   return b * st[0] + (t - b * a.N) * st[2];
 }
 
-// Rows h0 + (i0 + u) hs, u < kQkRows<T>, of one token's H rows (zeros past the end).
-template <typename T>
-__device__ __forceinline__ void load_rows(Raw8<T> (&x)[kQkRows<T>], bool act, const T* src,
-                                          int64_t sh, int H, int h0, int hs, int i0) {
+__device__ __forceinline__ int64_t position_of(const QkArgs& a, int64_t t) {
+  if (a.pos) return a.pos[t];
+  return a.pos0 + (t < a.N ? t : (int64_t)((uint32_t)t % (uint32_t)a.N));
+}
+
+// Rows of the heads h, h + hs, ... below H of one token, R of them (zeros past the end).
+template <typename T, int R>
+__device__ __forceinline__ void load_rows(Raw8<T> (&x)[R], bool act, const T* src, int64_t sh,
+                                          int H, int h, int hs, const LaneTurn& L) {
 #pragma unroll
-  for (int u = 0; u < kQkRows<T>; ++u) {
-    const int h = (i0 + u) * hs + h0;
+  for (int u = 0; u < R; ++u) {
     x[u].zero();
-    if (act && h < H) x[u].load(src + h * sh);
+    if (act && h + u * hs < H) x[u].load(src + (h + u * hs) * sh, L.e0, L.e1);
   }
 }
 
-// Norm and rotation of rows h0, h0 + hs, ... < H of one token: src + h sh -> dst + h dh.  `x` holds
-// the first rows; the rows after next are on their way while the present ones are turned.
+// Norm and rotation of the heads h0, h0 + hs, ... < H of one token: src + h sh -> dst + h dh.  `x`
+// holds the first rows.
 template <typename T, int LPR>
-__device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, int p, bool act,
-                                          Raw8<T> (&x)[kQkRows<T>], const T* src, int64_t sh, T* dst,
-                                          int64_t dh, int H, int h0, int hs, const void* w) {
-  float cw[8], sw[8];
-  {
-    float own[8], other[8];
-    load_weights<T>(w, 8 * p, a.d, own);
-    load_weights<T>(w, 8 * L.partner, a.d, other);
+__device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, bool act,
+                                          Raw8<T> (&x)[kQkRows<T>], const T* src, int64_t sh,
+                                          T* dst, int64_t dh, int H, int h0, int hs,
+                                          const void* w, bool in_row) {
+  constexpr int R = kQkRows<T>;
+  f2 cw[4], sw[4];
+  load_weights<T>(w, L, in_row, cw);
+  partners(cw, a.rope.interleaved, sw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cw[i] = own[i] * L.c[i];
-      sw[i] = (L.cross ? other[i] : own[i ^ 1]) * L.s[i];
-    }
+  for (int i = 0; i < 4; ++i) {
+    cw[i] = mul2(cw[i], L.c[i]);
+    sw[i] = mul2(sw[i], L.s[i]);
   }
   const float inv_d = 1.f / (float)a.d;
-  for (int i0 = 0; i0 * hs < H; i0 += kQkRows<T>) {
-    Raw8<T> ahead[kQkRows<T>];
-    load_rows<T>(ahead, act, src, sh, H, h0, hs, i0 + kQkRows<T>);
+  for (int hb = 0; hb < H; hb += R * hs) {   // (as many rounds for every lane of the warp)
+    const int h1 = hb + h0;
+    Raw8<T> ahead[R];
+    load_rows<T, R>(ahead, act, src, sh, H, h1 + R * hs, hs, L);
 #pragma unroll
-    for (int u = 0; u < kQkRows<T>; ++u) {
-      const int h = (i0 + u) * hs + h0;
-      float v[8], o[8];
+    for (int u = 0; u < R; ++u) {
+      const int h = h1 + u * hs;
+      f2 v[4], o[4];
       x[u].get(v);
-      float r = 1.f;
+      partners(v, a.rope.interleaved, o);
+      f2 r = pack2(1.f, 1.f);
       if (a.norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-        r = __frsqrt_rn(group_sum<LPR>(ss) * inv_d + a.eps);
-      }
-      if (L.cross) {
-        x[u].template from_lane<LPR>(L.partner).get(o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = v[i ^ 1];
+        const float t = rsqrtf(fmaf(group_dot<LPR>(v, v), inv_d, a.eps));
+        r = pack2(t, t);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = v[i] * cw[i];
-        v[i] = r * (L.on ? fmaf(o[i], sw[i], y) : y);
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], cw[i]);
+      if (L.on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fma2(o[i], sw[i], v[i]);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], r);
       if (act && h < H) {
         x[u].put(v);
-        x[u].store(dst + h * dh);
+        x[u].store(dst + h * dh, L.e0, L.e1);
       }
       x[u] = ahead[u];
     }
@@ -249,149 +310,142 @@ __global__ void __launch_bounds__(kQkThreads, kQkBlocks)
     }
     live = live && slot >= 0;
   }
-  const bool act = live && 8 * p < a.d;
-  int64_t position = 0;
-  if (live) position = a.pos ? (int64_t)a.pos[t] : a.pos0 + t % a.N;
+  constexpr int R = kQkRows<T>;
+  const bool in_row = 8 * p < a.d, act = live && in_row;
   const int64_t tt = live ? t : 0;
-  const T* q = static_cast<const T*>(a.q) + token_offset(a, a.qs, tt) + 8 * p;
-  const T* k = static_cast<const T*>(a.k) + token_offset(a, a.ks, tt) + 8 * p;
-  Raw8<T> x[kQkRows<T>];
-  load_rows<T>(x, act, q, a.qs[1], a.Hq, h0, hs, 0);
   LaneTurn L;
-  L.init(a.rope, p, live, position);
-  turn_rows<T, LPR>(a, L, p, act, x, q, a.qs[1],
-                    static_cast<T*>(a.qo) + token_offset(a, a.qos, tt) + 8 * p, a.qos[1], a.Hq,
-                    h0, hs, a.wq);
-  load_rows<T>(x, act, k, a.ks[1], a.Hkv, h0, hs, 0);
+  L.place(a.rope, p);
+  const T* q = static_cast<const T*>(a.q) + token_offset(a, a.qs, tt);
+  const T* k = static_cast<const T*>(a.k) + token_offset(a, a.ks, tt);
+  Raw8<T> x[R];
+  load_rows<T, R>(x, act, q, a.qs[1], a.Hq, h0, hs, L);
+  L.turn_to(a.rope, live ? position_of(a, t) : 0);
+  turn_rows<T, LPR>(a, L, act, x, q, a.qs[1],
+                    static_cast<T*>(a.qo) + token_offset(a, a.qos, tt), a.qos[1], a.Hq, h0, hs,
+                    a.wq, in_row);
+  load_rows<T, R>(x, act, k, a.ks[1], a.Hkv, h0, hs, L);
   if constexpr (PAGED) {
-    const int64_t page = live ? slot / a.page_size : 0;
-    const int64_t off = page * a.cs[0] + (live ? slot - page * a.page_size : 0) * a.cs[2] + 8 * p;
-    Raw8<T> y[kQkRows<T>];
-    const T* v = static_cast<const T*>(a.v) + token_offset(a, a.vs, tt) + 8 * p;
-    load_rows<T>(y, act, v, a.vs[1], a.Hkv, h0, hs, 0);
-    turn_rows<T, LPR>(a, L, p, act, x, k, a.ks[1], static_cast<T*>(a.Kc) + off, a.cs[1], a.Hkv,
-                      h0, hs, a.wk);
-    for (int i0 = 0; i0 * hs < a.Hkv; i0 += kQkRows<T>) {
-      if (i0 > 0) load_rows<T>(y, act, v, a.vs[1], a.Hkv, h0, hs, i0);
+    const uint32_t page = live ? (uint32_t)slot / (uint32_t)a.page_size : 0;
+    const int64_t off =
+        page * a.cs[0] + (live ? slot - (int64_t)page * a.page_size : 0) * a.cs[2];
+    Raw8<T> y[R];
+    const T* v = static_cast<const T*>(a.v) + token_offset(a, a.vs, tt);
+    load_rows<T, R>(y, act, v, a.vs[1], a.Hkv, h0, hs, L);
+    turn_rows<T, LPR>(a, L, act, x, k, a.ks[1], static_cast<T*>(a.Kc) + off, a.cs[1], a.Hkv, h0,
+                      hs, a.wk, in_row);
+    for (int h = h0; h < a.Hkv; h += R * hs) {
+      if (h > h0) load_rows<T, R>(y, act, v, a.vs[1], a.Hkv, h, hs, L);
 #pragma unroll
-      for (int u = 0; u < kQkRows<T>; ++u) {
-        const int h = (i0 + u) * hs + h0;
-        if (act && h < a.Hkv) y[u].store(static_cast<T*>(a.Vc) + off + h * a.cs[1]);
-      }
+      for (int u = 0; u < R; ++u)
+        if (act && h + u * hs < a.Hkv)
+          y[u].store(static_cast<T*>(a.Vc) + off + (h + u * hs) * a.cs[1], L.e0, L.e1);
     }
   } else {
-    turn_rows<T, LPR>(a, L, p, act, x, k, a.ks[1],
-                      static_cast<T*>(a.ko) + token_offset(a, a.kos, tt) + 8 * p, a.kos[1], a.Hkv,
-                      h0, hs, a.wk);
+    turn_rows<T, LPR>(a, L, act, x, k, a.ks[1],
+                      static_cast<T*>(a.ko) + token_offset(a, a.kos, tt), a.kos[1], a.Hkv, h0, hs,
+                      a.wk, in_row);
   }
 }
 
 // ---------------------------------------------------------------------------------- backward
 
-// Gradients of rows h0, h0 + hs, ... < H of one token; dw gains their share of this lane's eight
-// weight gradients.
+// Gradients of the heads h0, h0 + hs, ... < H of one token; dw gains their share of this lane's
+// eight weight gradients.
 template <typename T, typename GT, int LPR>
-__device__ __forceinline__ void grad_rows(const QkArgs& a, const LaneTurn& L, int p, bool act,
+__device__ __forceinline__ void grad_rows(const QkArgs& a, const LaneTurn& L, bool act,
                                           const T* src, int64_t sh, const GT* dy, int64_t gh,
                                           GT* dst, int64_t dh, int H, int h0, int hs,
-                                          const float (&w)[8], float (&dw)[8]) {
-  constexpr int U = 2;   // heads in flight together
+                                          const f2 (&w)[4], f2 (&dw)[4]) {
+  constexpr int R = kBwdRows;
   const float inv_d = 1.f / (float)a.d;
-  for (int hb = 0; hb < H; hb += hs * U) {
-    Raw8<T> xr[U];
-    Raw8<GT> gr[U];
+  const bool actx = act && a.norm;
+  Raw8<T> x[R];
+  Raw8<GT> g[R];
+  load_rows<T, R>(x, actx, src, sh, H, h0, hs, L);
+  load_rows<GT, R>(g, act, dy, gh, H, h0, hs, L);
+  for (int hb = 0; hb < H; hb += R * hs) {
+    const int h1 = hb + h0;
+    Raw8<T> xn[R];
+    Raw8<GT> gn[R];
+    load_rows<T, R>(xn, actx, src, sh, H, h1 + R * hs, hs, L);
+    load_rows<GT, R>(gn, act, dy, gh, H, h1 + R * hs, hs, L);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * hs + h0;
-      xr[u].zero();
-      gr[u].zero();
-      if (act && h < H) {
-        if (a.norm) xr[u].load(src + h * sh);
-        gr[u].load(dy + h * gh);
-      }
-    }
+    for (int u = 0; u < R; ++u) {
+      const int h = h1 + u * hs;
+      f2 v[4], o[4];
+      g[u].get(v);
+      if (L.on) {   // (turned back: L is at the negated position)
+        partners(v, a.rope.interleaved, o);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * hs + h0;
-      float x[8], g[8], o[8];
-      gr[u].get(g);
-      if (L.cross) {
-        gr[u].template from_lane<LPR>(L.partner).get(o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = g[i ^ 1];
-      }
-      if (L.on) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = fmaf(-o[i], L.s[i], g[i] * L.c[i]);
+        for (int i = 0; i < 4; ++i) v[i] = fma2(o[i], L.s[i], mul2(v[i], L.c[i]));
       }
       if (a.norm) {
-        xr[u].get(x);
-        float ss = 0.f, dot = 0.f;
+        f2 xv[4], wv[4];
+        x[u].get(xv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(x[i], x[i], ss);
-          dot = fmaf(g[i] * w[i], x[i], dot);
-        }
-        ss = group_sum<LPR>(ss);
-        dot = group_sum<LPR>(dot);
-        const float r = __frsqrt_rn(ss * inv_d + a.eps);
-        const float f = r * r * dot * inv_d;
+        for (int i = 0; i < 4; ++i) wv[i] = mul2(v[i], w[i]);
+        const float ss = group_dot<LPR>(xv, xv), dot = group_dot<LPR>(wv, xv);
+        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+        const float f = -r * r * dot * inv_d;
+        const f2 rr = pack2(r, r), ff = pack2(f, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw[i] = fmaf(g[i] * r, x[i], dw[i]);
-          g[i] = r * fmaf(-x[i], f, g[i] * w[i]);
+        for (int i = 0; i < 4; ++i) {
+          dw[i] = fma2(mul2(v[i], rr), xv[i], dw[i]);
+          v[i] = mul2(rr, fma2(xv[i], ff, wv[i]));
         }
       }
       if (act && h < H) {
-        gr[u].put(g);
-        gr[u].store(dst + h * dh);
+        g[u].put(v);
+        g[u].store(dst + h * dh, L.e0, L.e1);
       }
+      x[u] = xn[u];
+      g[u] = gn[u];
     }
   }
 }
 
+// Blocks walk the token groups; each leaves its lanes' shares of the weight gradients, added over
+// its lane groups, in dw_part.
 template <typename T, typename GT, int LPR>
-__global__ void __launch_bounds__(kQkThreads)
+__global__ void __launch_bounds__(kQkThreads, kBwdBlocks)
     qk_norm_rope_bwd_kernel(const __grid_constant__ QkArgs a, int tbl) {
   constexpr int NLG = kQkThreads / LPR;
   __shared__ float sDw[NLG][2][LPR * 8];
   const int lg = threadIdx.x / LPR, p = threadIdx.x % LPR;
   const int h0 = lg >> tbl, hs = NLG >> tbl;
-  float wq[8], wk[8], dwq[8], dwk[8];
-  load_weights<T>(a.wq, 8 * p, a.d, wq);
-  load_weights<T>(a.wk, 8 * p, a.d, wk);
+  const bool in_row = 8 * p < a.d;
+  LaneTurn L;
+  L.place(a.rope, p);
+  f2 wq[4], wk[4], dwq[4], dwk[4];
+  load_weights<T>(a.wq, L, in_row, wq);
+  load_weights<T>(a.wk, L, in_row, wk);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+  for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = 0ull;
   for (int64_t t0 = (int64_t)blockIdx.x << tbl; t0 < a.tokens; t0 += (int64_t)gridDim.x << tbl) {
     const int64_t t = t0 + (lg & ((1 << tbl) - 1));
-    const bool live = t < a.tokens;
-    const bool act = live && 8 * p < a.d;
-    int64_t position = 0;
-    if (live) position = a.pos ? (int64_t)a.pos[t] : a.pos0 + t % a.N;
-    LaneTurn L;
-    L.init(a.rope, p, live, position);
+    const bool live = t < a.tokens, act = live && in_row;
     const int64_t tt = live ? t : 0;
-    if (a.Hq > 0)
-      grad_rows<T, GT, LPR>(a, L, p, act,
-                            static_cast<const T*>(a.q) + token_offset(a, a.qs, tt) + 8 * p,
-                            a.qs[1],
-                            static_cast<const GT*>(a.gq) + token_offset(a, a.gqs, tt) + 8 * p,
-                            a.gqs[1], static_cast<GT*>(a.qo) + token_offset(a, a.qos, tt) + 8 * p,
-                            a.qos[1], a.Hq, h0, hs, wq, dwq);
-    if (a.Hkv > 0)
-      grad_rows<T, GT, LPR>(a, L, p, act,
-                            static_cast<const T*>(a.k) + token_offset(a, a.ks, tt) + 8 * p,
-                            a.ks[1],
-                            static_cast<const GT*>(a.gk) + token_offset(a, a.gks, tt) + 8 * p,
-                            a.gks[1], static_cast<GT*>(a.ko) + token_offset(a, a.kos, tt) + 8 * p,
-                            a.kos[1], a.Hkv, h0, hs, wk, dwk);
+    L.turn_to(a.rope, live ? -position_of(a, t) : 0);   // the transposed rotation turns back
+    grad_rows<T, GT, LPR>(a, L, act, static_cast<const T*>(a.q) + token_offset(a, a.qs, tt),
+                          a.qs[1], static_cast<const GT*>(a.gq) + token_offset(a, a.gqs, tt),
+                          a.gqs[1], static_cast<GT*>(a.qo) + token_offset(a, a.qos, tt),
+                          a.qos[1], a.Hq, h0, hs, wq, dwq);
+    grad_rows<T, GT, LPR>(a, L, act, static_cast<const T*>(a.k) + token_offset(a, a.ks, tt),
+                          a.ks[1], static_cast<const GT*>(a.gk) + token_offset(a, a.gks, tt),
+                          a.gks[1], static_cast<GT*>(a.ko) + token_offset(a, a.kos, tt),
+                          a.kos[1], a.Hkv, h0, hs, wk, dwk);
   }
   if (!a.dw_part) return;
+  if (in_row) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    sDw[lg][0][8 * p + i] = dwq[i];
-    sDw[lg][1][8 * p + i] = dwk[i];
+    for (int i = 0; i < 4; ++i) {
+      const int e = (i < 2 ? L.e0 : L.e1) + 2 * (i & 1);
+      const float2 u = unpack2(dwq[i]), v = unpack2(dwk[i]);
+      sDw[lg][0][e] = u.x;
+      sDw[lg][0][e + 1] = u.y;
+      sDw[lg][1][e] = v.x;
+      sDw[lg][1][e + 1] = v.y;
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < 2 * a.d; e += kQkThreads) {
