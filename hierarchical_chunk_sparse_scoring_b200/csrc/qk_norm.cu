@@ -28,9 +28,9 @@
 namespace hils {
 namespace {
 
-constexpr int kQkThreads = 256;
-constexpr int kQkBlocks = 3;    // blocks per SM (forward)
-constexpr int kBwdBlocks = 2;
+constexpr int kQkThreads = 128;
+constexpr int kQkBlocks = 5;    // blocks per SM (forward)
+constexpr int kBwdBlocks = 4;
 constexpr int kBwdRows = 2;     // heads of a lane group loaded together (backward)
 // heads of a lane group loaded together (forward); as many more are on their way
 template <typename T>
