@@ -19,16 +19,17 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sWarp, int64_t
   }
   if (lane == 31) sWarp[warp] = x;
   __syncthreads();
-  int64_t before = 0;
-  total = 0;
+  // every warp sums the warps itself
+  int64_t w = lane < NW ? sWarp[lane] : 0;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const int64_t y = sWarp[w];
-    if (w < warp) before += y;
-    total += y;
+  for (int o = 1; o < NW; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
+  total = __shfl_sync(0xffffffffu, w, NW - 1);
+  const int64_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
   __syncthreads();
-  return before + x - v;
+  return (warp ? before : 0) + x - v;
 }
 
 }  // namespace hils
