@@ -706,10 +706,13 @@ def paged_plan(kv_len, new_len, block_table, free_pages, n_free, *, page_size, T
         raise ValueError("T_cap must not be negative")
 
     def go(st):
-        slot, pos, seq = block_table.new_empty((3, T_cap)).unbind(0)
-        cu = block_table.new_empty(B + 1)
-        kv = torch.empty_like(kv_len) if kv_len_out is None else kv_len_out
-        nf = torch.empty_like(n_free) if n_free_out is None else n_free_out
+        # (one allocation: these live and die together)
+        slot, pos, seq, cu, kv, nf = block_table.new_empty(3 * T_cap + 2 * B + 2).split_with_sizes(
+            [T_cap, T_cap, T_cap, B + 1, B, 1])
+        if kv_len_out is not None:
+            kv = kv_len_out
+        if n_free_out is not None:
+            nf = n_free_out
         w = _workspace_of(ws, dev, 256)
         p = _PAGED.pack(T_cap, B, 0, 0, 0, P, M, 0, 0, 0, page_size, 0, 0, 0.0)
         _check(lib().hils_paged_plan(p, _addr(kv_len), _addr(new_len), _addr(block_table),

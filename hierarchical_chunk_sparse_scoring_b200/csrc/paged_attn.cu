@@ -24,6 +24,7 @@
 //         summed over the lanes by halving exchanges that leave each lane its own (head, token).
 #include "block_scan.cuh"
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "paged.h"
 
 namespace hils {
@@ -49,6 +50,7 @@ struct PaWs {
   PaRec* rec;    // [ctas]
   float* ml;     // [ctas][2][G][2] running maximum (base 2) and sum
   float* o;      // [ctas][2][G][d]
+  float* first;  // [ctas][8 warps][G][d], if shared memory does not hold them
 };
 
 __host__ __device__ inline size_t pa_align(size_t x) { return (x + 255) / 256 * 256; }
@@ -60,6 +62,8 @@ __host__ __device__ inline PaWs pa_carve(char* ws, int64_t G, int64_t d) {
   w.ml = reinterpret_cast<float*>(ws);
   ws += pa_align((size_t)kPaCtas * 2 * G * 2 * sizeof(float));
   w.o = reinterpret_cast<float*>(ws);
+  ws += pa_align((size_t)kPaCtas * 2 * G * d * sizeof(float));
+  w.first = reinterpret_cast<float*>(ws);
   return w;
 }
 
@@ -206,15 +210,20 @@ struct PaShape {
   static constexpr int CH = ROW / 16;                       // its 16-byte pieces
   static constexpr int HALF = KT * ROW;                     // K (or V) of a tile
   static constexpr int STAGE = 2 * HALF;
-  // warps and the bytes of each one's ring: what fits beside the parts (G D floats a warp)
-  static constexpr int NW = GM <= 4 || (GM <= 8 && sizeof(T) == 2) ? 8 : 6;
-  static constexpr int ST = (GM <= 8 && NW == 6 ? 32768 : 24576) / STAGE;
+  // Warps, and the stages of each one's ring.  The first part of a warp (G D floats) waits in
+  // shared memory where that fits beside the rings, else in the workspace.  (bf16 of 16 heads: six
+  // warps with their parts in shared memory beat eight with them in the workspace, 32 rows of
+  // 16384 tokens 61 us against 66 us; fp32, bound by instructions, wants the eight.)
+  static constexpr int NW = GM > 8 && sizeof(T) == 2 ? 6 : 8;
+  static constexpr int ST = 24576 / STAGE;
+  static constexpr bool FIRST_SMEM = GM <= 4 || sizeof(T) == 2 || (GM <= 8 && D == 64);
+  static constexpr int FIRST = FIRST_SMEM ? GM * D : 0;
   static constexpr int THREADS = NW * 32;
   static constexpr int SCRATCH = sizeof(T) == 2 ? 0 : KT * GM + GM;   // fp32: weights, factors
   static int smem(int G) {
-    return NW * ST * STAGE + NW * (G * D + 4 * G + SCRATCH) * (int)sizeof(float);
+    return NW * ST * STAGE + NW * ((FIRST_SMEM ? G * D : 0) + 4 * G + SCRATCH) * (int)sizeof(float);
   }
-  static_assert(NW * (ST * STAGE + (GM * D + 4 * GM + SCRATCH) * 4) + 1024 <= 227 * 1024,
+  static_assert(NW * (ST * STAGE + (FIRST + 4 * GM + SCRATCH) * 4) + 1024 <= 227 * 1024,
                 "fits an SM");
   static_assert(GM * D * 4 <= ST * STAGE, "a part fits a warp's ring");
   static_assert(ST >= 3, "two tiles in flight while one is used");
@@ -411,28 +420,18 @@ struct PaWarp<float, D, GM> {
   static constexpr int SPAN = V >= 32 ? 1 : 32 / V;    // lanes that hold the same logit
   static constexpr int LPH = 32 / GM;           // lanes that hold a head's logits
   static_assert(NV <= KG, "a lane's logits belong to one head");
-  float q[GM][EPL], o[GM][EPL], m, l;   // m, l: of head lane / LPH
+  static constexpr int PL = EPL / 2;            // ... in pairs
+  f2 q[GM][PL], o[GM][PL];
+  float m, l;                                   // of head lane / LPH
 
-  static __device__ __forceinline__ void get(float (&v)[EPL], const float* p) {
-    if constexpr (EPL == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(p);
-      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    } else {
-      const float2 t = *reinterpret_cast<const float2*>(p);
-      v[0] = t.x; v[1] = t.y;
-    }
-  }
-  static __device__ __forceinline__ void get_row(float (&v)[EPL], uint32_t addr) {
-    if constexpr (EPL == 4)
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+  static __device__ __forceinline__ void get_row(f2 (&v)[PL], uint32_t addr) {
+    if constexpr (PL == 2)
+      asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];"
+                   : "=l"(v[0]), "=l"(v[1])
                    : "r"(addr)
                    : "memory");
     else
-      asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];"
-                   : "=f"(v[0]), "=f"(v[1])
-                   : "r"(addr)
-                   : "memory");
+      asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v[0]) : "r"(addr) : "memory");
   }
   // one value per head (the scratch of GM > 1 lies on 16-byte boundaries)
   static __device__ __forceinline__ void get_heads(float (&v)[GM], const float* p) {
@@ -450,8 +449,10 @@ struct PaWarp<float, D, GM> {
 #pragma unroll
     for (int g = 0; g < GM; ++g) {
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) q[g][e] = 0.f;
-      if (g < G) get(q[g], src + g * D + lane * EPL);
+      for (int e = 0; e < PL; ++e) {
+        q[g][e] = 0ull;
+        if (g < G) q[g][e] = reinterpret_cast<const f2*>(src + g * D + lane * EPL)[e];
+      }
     }
   }
   __device__ __forceinline__ void reset() {
@@ -460,7 +461,7 @@ struct PaWarp<float, D, GM> {
 #pragma unroll
     for (int g = 0; g < GM; ++g)
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) o[g][e] = 0.f;
+      for (int e = 0; e < PL; ++e) o[g][e] = 0ull;
   }
   __device__ __forceinline__ void tile(uint32_t sK, uint32_t sV, uint32_t mask, float sc, int lane,
                                        float* scratch) {
@@ -471,14 +472,15 @@ struct PaWarp<float, D, GM> {
       float x[V];
 #pragma unroll
       for (int k = 0; k < KG; ++k) {
-        float kv[EPL];
+        f2 kv[PL];
         get_row(kv, sK + (k0 + k) * S::ROW + lane * EPL * 4);
 #pragma unroll
         for (int g = 0; g < GM; ++g) {
-          float t = 0.f;
+          f2 t = mul2(q[g][0], kv[0]);
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) t = fmaf(q[g][e], kv[e], t);
-          x[g * KG + k] = t;
+          for (int e = 1; e < PL; ++e) t = fma2(q[g][e], kv[e], t);
+          const float2 u = unpack2(t);
+          x[g * KG + k] = u.x + u.y;
         }
       }
       scatter_sum<V>(x, lane);
@@ -512,21 +514,21 @@ struct PaWarp<float, D, GM> {
       if (any) {
 #pragma unroll
         for (int g = 0; g < GM; ++g) {
-          const float r = sF[g];
+          const f2 r = pack2(sF[g], sF[g]);
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) o[g][e] *= r;
+          for (int e = 0; e < PL; ++e) o[g][e] = mul2(o[g][e], r);
         }
       }
 #pragma unroll
       for (int k = 0; k < KG; ++k) {
-        float vv[EPL];
+        f2 vv[PL];
         get_row(vv, sV + (k0 + k) * S::ROW + lane * EPL * 4);
         float w[GM];
         get_heads(w, sP + (k0 + k) * GM);
 #pragma unroll
         for (int g = 0; g < GM; ++g)
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) o[g][e] = fmaf(w[g], vv[e], o[g][e]);
+          for (int e = 0; e < PL; ++e) o[g][e] = fma2(pack2(w[g], w[g]), vv[e], o[g][e]);
       }
       __syncwarp();   // the scratch is written again
     }
@@ -545,12 +547,8 @@ struct PaWarp<float, D, GM> {
       const float f = __shfl_sync(0xffffffffu, inv, g * LPH);
       if (g < G) {
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) o[g][e] *= f;
-        if constexpr (EPL == 4)
-          *reinterpret_cast<float4*>(out + g * D + lane * EPL) =
-              make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
-        else
-          *reinterpret_cast<float2*>(out + g * D + lane * EPL) = make_float2(o[g][0], o[g][1]);
+        for (int e = 0; e < PL; ++e)
+          reinterpret_cast<f2*>(out + g * D + lane * EPL)[e] = mul2(o[g][e], pack2(f, f));
       }
     }
   }
@@ -565,7 +563,7 @@ struct PaWarp<float, D, GM> {
     for (int g = 0; g < GM; ++g) {
       if (g >= G) break;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) sO[g * D + lane * EPL + e] = o[g][e];
+      for (int e = 0; e < PL; ++e) reinterpret_cast<f2*>(sO + g * D + lane * EPL)[e] = o[g][e];
     }
   }
 };
@@ -665,12 +663,14 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
   const int G = a.G;
   uint8_t* ring = smem + warp * (ST * S::STAGE);
   float* sO = reinterpret_cast<float*>(smem + NW * ST * S::STAGE);   // [NW][G][D]
-  float* sM = sO + NW * G * D;                                   // [NW][2][G]
+  float* sM = sO + (S::FIRST_SMEM ? NW * G * D : 0);               // [NW][2][G]
   float* sL = sM + NW * 2 * G;
   float* scratch = sL + NW * 2 * G + warp * S::SCRATCH;
   bool bad = false;
   const PaPlan P = pa_schedule<NW, KT>(a, sStretch, bad);
   const PaWs W = pa_carve(a.ws, G, D);
+
+  float* const firsts_at = S::FIRST_SMEM ? sO : W.first + (int64_t)blockIdx.x * NW * G * D;
 
   // ---- copies of this warp's tiles.  Where the CTA's stretch lies in at most two units its tiles
   // go round the warps, so that the CTA reads consecutive rows (long rows: 563 us against 592 us
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
       // the first part waits beside the rings, the last one in this warp's own, then unused
       const int k = go ? 0 : 1;
       __syncwarp();
-      c.finish(go ? sO + warp * G * D : reinterpret_cast<float*>(ring),
+      c.finish(go ? firsts_at + warp * G * D : reinterpret_cast<float*>(ring),
                sM + (warp * 2 + k) * G, sL + (warp * 2 + k) * G, G, lane);
       if (lane == 0) sPart[warp][k] = PaPart{row, head, starts, ends};
     }
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(PaShape<T, D, GM>::THREADS, 1)
       const int o = __ffs(of) - 1;
       const float ro = __shfl_sync(0xffffffffu, r, o);
       const float* v = (o % 2 ? reinterpret_cast<const float*>(smem + (o / 2) * (ST * S::STAGE))
-                              : sO + (o / 2) * G * D) + g * D + lane * EPL;
+                              : firsts_at + (o / 2) * G * D) + g * D + lane * EPL;
 #pragma unroll
       for (int e = 0; e < EPL; ++e) O[e] = fmaf(ro, v[e], O[e]);
     }
@@ -961,9 +961,12 @@ cudaError_t launch_both(const PagedAttnArgs& a, cudaStream_t st) {
   const int64_t units = (int64_t)a.T * a.Hkv;
   // (launched early by programmatic dependent launch the join gained nothing: one row of 1000
   // tokens 11.0 us against 10.2 us)
-  if (units < grid - 1)
+  // (few units have many parts each: wide blocks while they all fit one per SM)
+  if (units * a.G <= grid)
     paged_attn_join_kernel<T, D, 1024, true>
         <<<dim3((unsigned)units, a.G), 1024, 0, st>>>(b, grid);
+  else if (units < grid - 1)
+    paged_attn_join_kernel<T, D, 256, true><<<dim3((unsigned)units, a.G), 256, 0, st>>>(b, grid);
   else
     paged_attn_join_kernel<T, D, 256, false><<<dim3(grid - 1, a.G), 256, 0, st>>>(b, grid);
   return cudaGetLastError();
@@ -975,8 +978,9 @@ bool paged_attn_supported(int64_t d, int64_t G) { return (d == 64 || d == 128) &
 
 size_t paged_attn_ws(int64_t d, int64_t G) {
   const PaWs w = pa_carve(nullptr, G, d);
-  return reinterpret_cast<size_t>(w.o) +
-         pa_align((size_t)kPaCtas * 2 * G * d * sizeof(float));
+  // (first parts: wherever a kernel for more than four heads may leave them there)
+  return reinterpret_cast<size_t>(w.first) +
+         (G > 4 ? pa_align((size_t)kPaCtas * 8 * G * d * sizeof(float)) : 0);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool bf16, cudaStream_t st) {

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "qk_norm.h"
 
 namespace hils {
@@ -35,29 +36,6 @@ constexpr int kBwdRows = 2;     // heads of a lane group loaded together (backwa
 // heads of a lane group loaded together (forward); as many more are on their way
 template <typename T>
 constexpr int kQkRows = sizeof(T) == 2 ? 4 : 2;
-
-// ---- two fp32 numbers in one register pair
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(f2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 // A lane's eight elements as they are stored: pieces of four at element offsets e0 and e1.
 template <typename T>
