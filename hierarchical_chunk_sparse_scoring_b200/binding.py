@@ -616,6 +616,9 @@ def qk_norm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, rope, *, pos=None, pos
     dk (in the gradients' dtype; dq may be dq_out) and dw_q, dw_k (fp32 [d], None where there is
     no weight)."""
     dev, dt, dims, sq, sk = _qk_setup(q, k, w_q, w_k, pos)
+    for x, dy, n in ((q, dq_out, "dq_out"), (k, dk_out, "dk_out")):
+        if x is not None and not isinstance(dy, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % n)
     gt = (dq_out if q is not None else dk_out).dtype
 
     def go(st):

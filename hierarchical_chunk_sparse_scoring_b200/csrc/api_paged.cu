@@ -341,7 +341,8 @@ extern "C" hils_status hils_paged_attn(const hils_paged_params* p, const void* q
   if (!any) return HILS_OK;
   if ((s = check_device()) != HILS_OK) return s;
   PagedAttnArgs a;
-  a.q = q; a.K = K; a.V = V; a.table = block_table; a.seq = seq; a.pos = pos;
+  // (an empty pool has no address; copies of nothing still name one)
+  a.q = q; a.K = pool ? K : q; a.V = pool ? V : q; a.table = block_table; a.seq = seq; a.pos = pos;
   a.out = out; a.lse = lse;
   copy3(a.cs, p->c_str);
   a.max_pages = p->max_pages;

@@ -383,8 +383,9 @@ hils_status hils_paged_append(const hils_qk_params* p, const hils_rope* rope,
  * recorded.  A row with seq[t] < 0 is padding, left as it was.  The work is split evenly over the
  * SMs along the rows' lengths and joined in a fixed order, so a call repeats bit for bit (where a
  * row is split, and with it its last bits, depends on the other rows' lengths); the launches do not depend on the lengths, so a step can be captured in a CUDA graph.  Supported:
- * d = 64 or 128, G = Hq / Hkv <= 16.  bf16: products on the tensor cores, softmax weights rounded
- * to bf16 for the product with V, sums fp32; fp32: all fp32.
+ * d = 64 or 128, G = Hq / Hkv <= 16.  bf16: products on the tensor cores, softmax weights carried
+ * as two bf16 (16 bits) for the product with V, sums fp32; fp32: all fp32.  A row whose every
+ * logit is -inf gives out 0, lse -inf.
  */
 hils_status hils_paged_attn(const hils_paged_params* p, const void* q, const void* K,
                             const void* V, const int32_t* block_table, const int32_t* seq,

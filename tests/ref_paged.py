@@ -91,7 +91,8 @@ def attention(q, K, V, lo, hi, scale, weights_dtype):
     """One row: q [Hq, d] over K, V [n, Hkv, d] tokens lo .. hi - 1.  (out, lse, out bound, lse
     bound).  A logit is within (d + 4) u sum|q k| scale, its weight within that, the exponent's
     rounding (2 u |x - m|) and 4 u relative; sums over tokens add at most n/8 + 64 roundings (eight
-    warps take the tiles in turn); bf16 rounds each weight once for the product with V."""
+    warps take the tiles in turn); bf16 carries each weight as two bf16 for the product with V, half
+    a step of half a step, 2^-16."""
     Hq, d = q.shape
     n, Hkv, _ = K.shape
     if hi <= lo:
@@ -107,7 +108,7 @@ def attention(q, K, V, lo, hi, scale, weights_dtype):
     far = (x.amax(-1, keepdim=True) - x).clamp(max=80.0)
     e = ((d + 4) * U * mag + 2 * U * far + 4 * U).amax(-1)
     sums = ((hi - lo) / 8 + 64) * U
-    rounded = HALF_STEP[weights_dtype] if weights_dtype == torch.bfloat16 else 0.0
+    rounded = 2.0 ** -16 if weights_dtype == torch.bfloat16 else 0.0
     out_b = (2 * e[:, None] + 2 * sums + rounded) * pv
     return out, lse, out_b, e + sums + 4 * U * lse.abs()
 

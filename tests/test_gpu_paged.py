@@ -359,6 +359,46 @@ def test_attn_empty_and_refusals():
                       V[..., :32].contiguous(), table, pos)
 
 
+def test_attn_many_short_rows_and_one_head_rows():
+    """More units than blocks, most of one tile, some cut, some empty, rows of other sequences."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 40, (700,), generator=g).tolist()
+    lens[10] = lens[650] = 5000
+    for dtype in (BF, F32):
+        c = attn_case(lens, 4, 2, 64, 8, dtype, seed=1)
+        out, lse = hb.paged_attn(*c)
+        check_attn(*c, out, lse, rows=[0, 1, 9, 10, 11, 300, 649, 650, 651, 699])
+        # every row against the batch of itself alone: another split, the same value
+        for t in range(0, 700, 97):
+            o, z = hb.paged_attn(c[0][t:t + 1].contiguous(), c[1], c[2], c[3][t:t + 1].contiguous(),
+                                 c[4][t:t + 1].contiguous())
+            check_attn(c[0][t:t + 1], c[1], c[2], c[3][t:t + 1], c[4][t:t + 1], o, z)
+
+
+def test_attn_of_an_empty_pool_and_table():
+    q = torch.randn((3, 4, 64), device="cuda")
+    K = torch.empty((0, 2, 16, 64), device="cuda")
+    ws = hb.paged_workspace(q, K)
+    table = torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    out, lse = hb.paged_attn(q, K, K.clone(), table, ints([-1, 5, 31]), ws=ws)
+    assert hb.device_status(ws) == 5
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    out, lse = hb.paged_attn(q, K, K.clone(), table[:, :0].contiguous(), ints([-1, -1, -1]), ws=ws)
+    assert hb.device_status(ws) == 0 and bool((out == 0).all())
+
+
+def test_one_workspace_serves_calls_in_turn():
+    """Plan, append and attention of several shapes on one workspace, one after another."""
+    big = attn_case([3000, 40], 16, 1, 128, 64, BF, seed=2)
+    ws = hb.paged_workspace(big[0], big[1])
+    for c in (big, attn_case([7, 900, 0], 8, 4, 64, 16, F32, seed=3), big):
+        out, lse = hb.paged_attn(*c, ws=ws)
+        check_attn(*c, out, lse)
+        hb.paged_plan(ints([1]), ints([1]), ints([[0]]), ints([1]), ints([1]), page_size=8,
+                      T_cap=1, ws=ws)
+        assert hb.device_status(ws) == 0
+
+
 # ----------------------------------------------------------------------------- used together
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
