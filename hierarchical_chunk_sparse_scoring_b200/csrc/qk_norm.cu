@@ -114,10 +114,11 @@ __device__ __forceinline__ float group_dot(const f2 (&a)[4], const f2 (&b)[4]) {
 }
 
 // The partners of a lane's elements, in the same order.
-__device__ __forceinline__ void partners(const f2 (&v)[4], bool interleaved, f2 (&o)[4]) {
+template <bool IL>   // interleaved layout (else half)
+__device__ __forceinline__ void partners(const f2 (&v)[4], f2 (&o)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (interleaved) {
+    if constexpr (IL) {
       const float2 t = unpack2(v[i]);
       o[i] = pack2(t.y, t.x);
     } else {
@@ -222,7 +223,7 @@ __device__ __forceinline__ void load_rows(Raw8<T> (&x)[R], bool act, const T* sr
 
 // Norm and rotation of the heads h0, h0 + hs, ... < H of one token: src + h sh -> dst + h dh.  `x`
 // holds the first rows.
-template <typename T, int LPR>
+template <typename T, int LPR, bool IL>
 __device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, bool act,
                                           Raw8<T> (&x)[kQkRows<T>], const T* src, int64_t sh,
                                           T* dst, int64_t dh, int H, int h0, int hs,
@@ -230,7 +231,7 @@ __device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, bo
   constexpr int R = kQkRows<T>;
   f2 cw[4], sw[4];
   load_weights<T>(w, L, in_row, cw);
-  partners(cw, a.rope.interleaved, sw);
+  partners<IL>(cw, sw);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     cw[i] = mul2(cw[i], L.c[i]);
@@ -246,7 +247,7 @@ __device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, bo
       const int h = h1 + u * hs;
       f2 v[4], o[4];
       x[u].get(v);
-      partners(v, a.rope.interleaved, o);
+      partners<IL>(v, o);
       f2 r = pack2(1.f, 1.f);
       if (a.norm) {
         const float t = rsqrtf(fmaf(group_dot<LPR>(v, v), inv_d, a.eps));
@@ -271,7 +272,7 @@ __device__ __forceinline__ void turn_rows(const QkArgs& a, const LaneTurn& L, bo
 
 // grid: blocks of 2^tbl tokens; a lane group holds token (group mod 2^tbl) and the heads
 // (group / 2^tbl) mod the groups per token.
-template <typename T, int LPR, bool PAGED>
+template <typename T, int LPR, bool IL, bool PAGED>
 __global__ void __launch_bounds__(kQkThreads, kQkBlocks)
     qk_norm_rope_kernel(const __grid_constant__ QkArgs a, int tbl) {
   constexpr int NLG = kQkThreads / LPR;
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBlocks)
   Raw8<T> x[R];
   load_rows<T, R>(x, act, q, a.qs[1], a.Hq, h0, hs, L);
   L.turn_to(a.rope, live ? position_of(a, t) : 0);
-  turn_rows<T, LPR>(a, L, act, x, q, a.qs[1],
+  turn_rows<T, LPR, IL>(a, L, act, x, q, a.qs[1],
                     static_cast<T*>(a.qo) + token_offset(a, a.qos, tt), a.qos[1], a.Hq, h0, hs,
                     a.wq, in_row);
   load_rows<T, R>(x, act, k, a.ks[1], a.Hkv, h0, hs, L);
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBlocks)
     Raw8<T> y[R];
     const T* v = static_cast<const T*>(a.v) + token_offset(a, a.vs, tt);
     load_rows<T, R>(y, act, v, a.vs[1], a.Hkv, h0, hs, L);
-    turn_rows<T, LPR>(a, L, act, x, k, a.ks[1], static_cast<T*>(a.Kc) + off, a.cs[1], a.Hkv, h0,
+    turn_rows<T, LPR, IL>(a, L, act, x, k, a.ks[1], static_cast<T*>(a.Kc) + off, a.cs[1], a.Hkv, h0,
                       hs, a.wk, in_row);
     for (int h = h0; h < a.Hkv; h += R * hs) {
       if (h > h0) load_rows<T, R>(y, act, v, a.vs[1], a.Hkv, h, hs, L);
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBlocks)
           y[u].store(static_cast<T*>(a.Vc) + off + (h + u * hs) * a.cs[1], L.e0, L.e1);
     }
   } else {
-    turn_rows<T, LPR>(a, L, act, x, k, a.ks[1],
+    turn_rows<T, LPR, IL>(a, L, act, x, k, a.ks[1],
                       static_cast<T*>(a.ko) + token_offset(a, a.kos, tt), a.kos[1], a.Hkv, h0, hs,
                       a.wk, in_row);
   }
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBlocks)
 
 // Gradients of the heads h0, h0 + hs, ... < H of one token; dw gains their share of this lane's
 // eight weight gradients.
-template <typename T, typename GT, int LPR>
+template <typename T, typename GT, int LPR, bool IL>
 __device__ __forceinline__ void grad_rows(const QkArgs& a, const LaneTurn& L, bool act,
                                           const T* src, int64_t sh, const GT* dy, int64_t gh,
                                           GT* dst, int64_t dh, int H, int h0, int hs,
@@ -353,7 +354,7 @@ __device__ __forceinline__ void grad_rows(const QkArgs& a, const LaneTurn& L, bo
       f2 v[4], o[4];
       g[u].get(v);
       if (L.on) {   // (turned back: L is at the negated position)
-        partners(v, a.rope.interleaved, o);
+        partners<IL>(v, o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = fma2(o[i], L.s[i], mul2(v[i], L.c[i]));
       }
@@ -384,7 +385,7 @@ __device__ __forceinline__ void grad_rows(const QkArgs& a, const LaneTurn& L, bo
 
 // Blocks walk the token groups; each leaves its lanes' shares of the weight gradients, added over
 // its lane groups, in dw_part.
-template <typename T, typename GT, int LPR>
+template <typename T, typename GT, int LPR, bool IL>
 __global__ void __launch_bounds__(kQkThreads, kBwdBlocks)
     qk_norm_rope_bwd_kernel(const __grid_constant__ QkArgs a, int tbl) {
   constexpr int NLG = kQkThreads / LPR;
@@ -404,11 +405,11 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocks)
     const bool live = t < a.tokens, act = live && in_row;
     const int64_t tt = live ? t : 0;
     L.turn_to(a.rope, live ? -position_of(a, t) : 0);   // the transposed rotation turns back
-    grad_rows<T, GT, LPR>(a, L, act, static_cast<const T*>(a.q) + token_offset(a, a.qs, tt),
+    grad_rows<T, GT, LPR, IL>(a, L, act, static_cast<const T*>(a.q) + token_offset(a, a.qs, tt),
                           a.qs[1], static_cast<const GT*>(a.gq) + token_offset(a, a.gqs, tt),
                           a.gqs[1], static_cast<GT*>(a.qo) + token_offset(a, a.qos, tt),
                           a.qos[1], a.Hq, h0, hs, wq, dwq);
-    grad_rows<T, GT, LPR>(a, L, act, static_cast<const T*>(a.k) + token_offset(a, a.ks, tt),
+    grad_rows<T, GT, LPR, IL>(a, L, act, static_cast<const T*>(a.k) + token_offset(a, a.ks, tt),
                           a.ks[1], static_cast<const GT*>(a.gk) + token_offset(a, a.gks, tt),
                           a.gks[1], static_cast<GT*>(a.ko) + token_offset(a, a.kos, tt),
                           a.kos[1], a.Hkv, h0, hs, wk, dwk);
@@ -477,10 +478,11 @@ cudaError_t launch_fwd(const QkArgs& a, bool paged, cudaStream_t st) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int tbl = tokens_log2(a.tokens, kQkThreads / LPR, sms);
   const int64_t grid = (a.tokens + (1 << tbl) - 1) >> tbl;
-  if (paged)
-    qk_norm_rope_kernel<T, LPR, true><<<(unsigned)grid, kQkThreads, 0, st>>>(a, tbl);
-  else
-    qk_norm_rope_kernel<T, LPR, false><<<(unsigned)grid, kQkThreads, 0, st>>>(a, tbl);
+  auto kern = a.rope.interleaved ? (paged ? qk_norm_rope_kernel<T, LPR, true, true>
+                                          : qk_norm_rope_kernel<T, LPR, true, false>)
+                                 : (paged ? qk_norm_rope_kernel<T, LPR, false, true>
+                                          : qk_norm_rope_kernel<T, LPR, false, false>);
+  kern<<<(unsigned)grid, kQkThreads, 0, st>>>(a, tbl);
   return cudaGetLastError();
 }
 
@@ -491,8 +493,9 @@ cudaError_t launch_bwd(const QkArgs& a, float* dw_q, float* dw_k, cudaStream_t s
   const int tbl = tokens_log2(a.tokens, kQkThreads / LPR, sms);
   int64_t grid = (a.tokens + (1 << tbl) - 1) >> tbl;
   if (grid > kQkBwdBlocks) grid = kQkBwdBlocks;
-  if (grid > 0)
-    qk_norm_rope_bwd_kernel<T, GT, LPR><<<(unsigned)grid, kQkThreads, 0, st>>>(a, tbl);
+  auto kern = a.rope.interleaved ? qk_norm_rope_bwd_kernel<T, GT, LPR, true>
+                                 : qk_norm_rope_bwd_kernel<T, GT, LPR, false>;
+  if (grid > 0) kern<<<(unsigned)grid, kQkThreads, 0, st>>>(a, tbl);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.dw_part) return e;
   qk_dw_join_kernel<<<(2 * a.d + 31) / 32, 1024, 0, st>>>(a.dw_part, (int)grid, a.d, dw_q, dw_k);
