@@ -9,9 +9,9 @@
 // dx = r (w g - x r^2 mean(w g x)).
 //
 // Bound: HBM, and close behind it instruction issue: a row of 128 bf16 is read and written once
-// (512 bytes, 12 ns of one SM's share of HBM), so that about 140 instructions for a warp's step of
-// two rows already take as long as the copies (125 us for 32768 tokens of 40 heads, floor 104 us).
-// Hence:
+// (512 bytes, 12 ns of one SM's share of HBM), so that 140 instructions for a warp's step of two
+// rows already take as long as the copies.  (32768 tokens of 40 heads: 119 us, 5.7 TB/s, issue
+// slots 62% used; the copies alone 104 us.)  Hence:
 //   - a lane holds eight elements as two pieces of four, which in the half layout are both members
 //     of four pairs (dims 4p .. and rot/2 + 4p ..): a rotation never leaves its lane, and the only
 //     exchange is the sum of squares over the row's LPR lanes (8, 16 or 32 by the head dim);
@@ -29,11 +29,15 @@
 namespace hils {
 namespace {
 
+// Blocks per SM and heads that a lane group loads together (as many more are on their way): what
+// the registers hold.  32768 tokens of 40 heads, 128 bf16, forward / 16301 tokens, append:
+// 119 / 74 us; two heads at eight blocks 126 / 81, six blocks (spilling) 121 / 84; 256 threads
+// and three blocks, whose ends leave more of an SM idle, 125 / 89.  Backward of 2 x 8192 tokens:
+// 146 us; one head 176, five blocks 186.
 constexpr int kQkThreads = 128;
-constexpr int kQkBlocks = 5;    // blocks per SM (forward)
+constexpr int kQkBlocks = 5;    // forward
 constexpr int kBwdBlocks = 4;
-constexpr int kBwdRows = 2;     // heads of a lane group loaded together (backward)
-// heads of a lane group loaded together (forward); as many more are on their way
+constexpr int kBwdRows = 2;
 template <typename T>
 constexpr int kQkRows = sizeof(T) == 2 ? 4 : 2;
 
