@@ -30,6 +30,7 @@
 #include "block_scan.cuh"
 #include "common.cuh"
 #include "f32x2.cuh"
+#include "host.h"
 #include "paged.h"
 
 namespace hils {
@@ -951,10 +952,9 @@ cudaError_t launch_one(const PagedAttnArgs& a, int grid, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t launch_both(const PagedAttnArgs& a, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  cudaError_t e;
   const int grid = sms < kPaCtas ? sms : kPaCtas;
   PagedAttnArgs b = a;
   b.inv_ctas = 1.0 / grid;

@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
       a.n_free_out[0] = free_n - n_new;
     }
   }
-  for (int x = me; x < n_new; x += stride) {
-    const int b = find(sPg, a.B, x);
+  for (int64_t y = me; y < n_new; y += stride) {
+    const int x = (int)y, b = find(sPg, a.B, x);
     a.table[b * a.max_pages + sHave[b] + (x - sPg[b])] = a.free_pages[free_n - 1 - x];
   }
   for (int64_t t0 = me; t0 < a.T; t0 += (int64_t)kPlanBatch * stride) {

@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "f32x2.cuh"
+#include "host.h"
 #include "qk_norm.h"
 
 namespace hils {
@@ -460,14 +461,6 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 // Tokens of a block, log2: as many as it has lane groups, halved while the grid would leave SMs
 // without two blocks (a few tokens then spread their heads over the lane groups instead).
 int tokens_log2(int64_t tokens, int groups, int sms) {
@@ -478,7 +471,7 @@ int tokens_log2(int64_t tokens, int groups, int sms) {
 
 template <typename T, int LPR>
 cudaError_t launch_fwd(const QkArgs& a, bool paged, cudaStream_t st) {
-  const int sms = sm_count();
+  const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int tbl = tokens_log2(a.tokens, kQkThreads / LPR, sms);
   const int64_t grid = (a.tokens + (1 << tbl) - 1) >> tbl;
@@ -492,7 +485,7 @@ cudaError_t launch_fwd(const QkArgs& a, bool paged, cudaStream_t st) {
 
 template <typename T, typename GT, int LPR>
 cudaError_t launch_bwd(const QkArgs& a, float* dw_q, float* dw_k, cudaStream_t st) {
-  const int sms = sm_count();
+  const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int tbl = tokens_log2(a.tokens, kQkThreads / LPR, sms);
   int64_t grid = (a.tokens + (1 << tbl) - 1) >> tbl;

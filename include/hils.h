@@ -345,7 +345,7 @@ size_t hils_paged_workspace_size(const hils_paged_params* p);
  * numbered in order of (b, position), token t < cu[B]:  seq[t] = b, pos[t] = its position,
  * slot[t] = its slot; tokens cu[B] .. T - 1 get -1 in all three.  cu [B + 1] counts the tokens
  * before each sequence; kv_len_out = kv_len + new_len and n_free_out the pages left, each may be
- * its input (in place).  A sequence is refused (no tokens, no pages, length kept, recorded in the
+ * its input (in place); no other arrays of the call may overlap.  A sequence is refused (no tokens, no pages, length kept, recorded in the
  * status word) if a length is negative, if it would outgrow max_pages, or if the tokens or pages
  * asked for up to and including it exceed T or the free pages (one that needs no new page is not
  * refused for pages).  A page id outside the pool gives slot -1 and is recorded.  Reads T, B,
