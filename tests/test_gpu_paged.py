@@ -387,6 +387,44 @@ def test_attn_of_an_empty_pool_and_table():
     assert hb.device_status(ws) == 0 and bool((out == 0).all())
 
 
+def test_offsets_past_32_bits():
+    """Pools of more than 2^31 elements, the pages in use at their far end: append, then read."""
+    Hkv, page, d, P = 8, 64, 128, 33000
+    assert P * Hkv * page * d > 2 ** 31
+    K, V = [torch.empty((P, Hkv, page, d), dtype=BF, device="cuda") for _ in range(2)]
+    g = gen(21)
+    n = 200
+    table = ints([[P - 1, 3, P - 2, P - 3]])
+    j = torch.arange(n, device="cuda")
+    slot = (table[0].long()[j // page] * page + j % page).to(torch.int32)
+    x = torch.randn((n, 32 + 2 * Hkv, d), generator=g, device="cuda").to(BF)
+    rope, ws = hb.rope(d), hb.paged_workspace(x[:1, :32], K)
+    w = torch.ones(d, dtype=BF, device="cuda")
+    q = hb.paged_append(x[:, :32], x[:, 32:40], x[:, 40:], w, w, rope, K, V, j.to(torch.int32),
+                        slot, ws=ws)
+    pos = ints([n - 1])
+    out, lse = hb.paged_attn(q[-1:].contiguous(), K, V, table, pos, ws=ws)
+    assert hb.device_status(ws) == 0
+    s = slot.long()
+    assert torch.equal(V[s // page, :, s % page], x[:, 40:])
+    check_attn(q[-1:], K, V, table, pos, out, lse)
+
+
+def test_two_streams_at_once():
+    cases = [attn_case([4000, 9, 700], 8, 2, 128, 64, BF, seed=31),
+             attn_case([100] * 40 + [3000], 16, 16, 64, 16, F32, seed=32)]
+    want = [hb.paged_attn(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    wss = [hb.paged_workspace(c[0], c[1]) for c in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        got += [hb.paged_attn(*c, stream=s, ws=w) for c, s, w in zip(cases, streams, wss)]
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
 def test_one_workspace_serves_calls_in_turn():
     """Plan, append and attention of several shapes on one workspace, one after another."""
     big = attn_case([3000, 40], 16, 1, 128, 64, BF, seed=2)

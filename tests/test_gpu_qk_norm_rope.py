@@ -221,6 +221,23 @@ def test_stream_and_graph():
             assert torch.equal(b[n], grads[n])
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last tokens as in a short call of their own, both directions."""
+    N, H, d = 530000, 32, 128
+    assert N * H * d > 2 ** 31
+    q = torch.empty((1, N, H, d), dtype=BF, device="cuda").normal_(
+        generator=torch.Generator(device="cuda").manual_seed(1)).transpose(1, 2)
+    w = torch.ones(d, dtype=BF, device="cuda")
+    rope = hb.rope(d, scaling="linear", factor=4.0)
+    tail = q[:, :, -7:]
+    want, _ = hb.qk_norm_rope(tail, None, w, None, rope, pos0=N - 7)
+    got, _ = hb.qk_norm_rope(q, None, w, None, rope)
+    assert torch.equal(got[:, :, -7:], want)
+    want = hb.qk_norm_rope_backward(tail, None, w, None, got[:, :, -7:], None, rope, pos0=N - 7)
+    dq = hb.qk_norm_rope_backward(q, None, w, None, got, None, rope, dq=got)["dq"]
+    assert torch.equal(dq[:, :, -7:], want["dq"])
+
+
 def test_empty():
     rope = hb.rope(64)
     q = torch.empty((2, 4, 0, 64), device="cuda")
