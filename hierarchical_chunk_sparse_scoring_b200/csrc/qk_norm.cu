@@ -369,7 +369,8 @@ __device__ __forceinline__ void grad_rows(const QkArgs& a, const LaneTurn& L, bo
 #pragma unroll
         for (int i = 0; i < 4; ++i) wv[i] = mul2(v[i], w[i]);
         const float ss = group_dot<LPR>(xv, xv), dot = group_dot<LPR>(wv, xv);
-        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+        // (places without a row hold zeros: without eps their norm would be infinite)
+        const float r = act && h < H ? rsqrtf(fmaf(ss, inv_d, a.eps)) : 0.f;
         const float f = -r * r * dot * inv_d;
         const f2 rr = pack2(r, r), ff = pack2(f, f);
 #pragma unroll
