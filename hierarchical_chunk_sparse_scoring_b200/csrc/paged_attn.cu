@@ -236,6 +236,25 @@ struct PaShape {
   static_assert(CH == 8 || CH == 16 || CH == 32, "whole rows per copy");
 };
 
+// A softmax weight w > 0 as three numbers >= 0 whose upper 16 bits, as bf16, add up to it: eight bits
+// of the mantissa each, cut off and not rounded, so that none is negative.  A part that would be
+// zero is w 2^-30 instead, which changes the sum by less than its rounding: with all three above
+// zero an infinite value times the weight is that infinity (a weight from 2^-96 on, below which the
+// small part has no normal bf16), where parts of both signs or zero would give NaN.
+__device__ __forceinline__ float upper16(float x) {
+  return __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+}
+__device__ __forceinline__ void split_weight(float w, float (&part)[3]) {
+  const float least = w * 0x1p-30f;
+  part[0] = w;
+  part[1] = fmaxf(w - upper16(w), least);
+  part[2] = fmaxf(part[1] - upper16(part[1]), least);
+}
+// The upper 16 bits of two numbers, a's below.
+__device__ __forceinline__ uint32_t pack_upper16(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
 // The softmax and products of one warp over its tiles of a unit.  load(q) reads the unit's
 // queries, tile() takes one tile, finish() leaves (m, sum, O) of every head in shared memory.
 template <typename T, int D, int GM>
@@ -289,10 +308,10 @@ struct PaWarp<__nv_bfloat16, D, GM> {
       for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], a, q[nb][k][0], q[nb][k][1]);
     }
     const bool see0 = (mask >> (lane / 4)) & 1, see1 = (mask >> (lane / 4 + 8)) & 1;
-    // The weights as two bf16 each (16 bits of their mantissa): one alone would add as much error
-    // as the rounding of the output.  The second product costs nothing up to 8 heads (573 us
-    // either way for 8 rows of 120K tokens) and a tenth with 16.
-    uint32_t p[NB][2], p2[NB][2];
+    // The weights as three bf16 each, all 24 bits of them.  (One alone would add as much error as the
+    // rounding of the output, two leave 16 bits.  Three cost nothing: 64 ragged rows 181 us with two
+    // or three, 32 rows of 16384 tokens and 16 heads 79 us either way with a cold cache.)
+    uint32_t p[NB][3][2];
     float f[NB][2];
     bool moved = false;
 #pragma unroll
@@ -319,12 +338,11 @@ struct PaWarp<__nv_bfloat16, D, GM> {
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const __nv_bfloat162 w = __floats2bfloat162_rn(s[nb][2 * h], s[nb][2 * h + 1]);
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(&w);
-        const __nv_bfloat162 w2 = __floats2bfloat162_rn(s[nb][2 * h] - bf16_lo(u),
-                                                        s[nb][2 * h + 1] - bf16_hi(u));
-        p[nb][h] = transpose8x8(u);
-        p2[nb][h] = transpose8x8(*reinterpret_cast<const uint32_t*>(&w2));
+        float a[3], b[3];
+        split_weight(s[nb][2 * h], a);
+        split_weight(s[nb][2 * h + 1], b);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) p[nb][k][h] = transpose8x8(pack_upper16(a[k], b[k]));
       }
     }
     if (__any_sync(0xffffffffu, moved)) {
@@ -342,8 +360,8 @@ struct PaWarp<__nv_bfloat16, D, GM> {
       ldsm4_t(a, sV + r * S::ROW + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        mma16816(o[nb][i], a, p[nb][0], p[nb][1]);
-        mma16816(o[nb][i], a, p2[nb][0], p2[nb][1]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) mma16816(o[nb][i], a, p[nb][k][0], p[nb][k][1]);
       }
     }
   }

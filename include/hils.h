@@ -384,7 +384,8 @@ hils_status hils_paged_append(const hils_qk_params* p, const hils_rope* rope,
  * SMs along the rows' lengths and joined in a fixed order, so a call repeats bit for bit (where a
  * row is split, and with it its last bits, depends on the other rows' lengths); the launches do not depend on the lengths, so a step can be captured in a CUDA graph.  Supported:
  * d = 64 or 128, G = Hq / Hkv <= 16.  bf16: products on the tensor cores, softmax weights carried
- * as two bf16 (16 bits) for the product with V, sums fp32; fp32: all fp32.  A row whose every
+ * as three bf16 (all of their 24 bits) for the product with V, sums fp32; fp32: all fp32.  An
+ * infinite value that a row sees with a weight of at least 2^-96 of its largest is in its output.  A row whose every
  * logit is -inf gives out 0, lse -inf.
  */
 hils_status hils_paged_attn(const hils_paged_params* p, const void* q, const void* K,

@@ -1,0 +1,72 @@
+"""Edges of the paged cache's operators: infinities that a row sees, weights below 16 bits, tiles at
+every cut of the split, empty pools, steps of many tokens."""
+import math
+
+import pytest
+import torch
+
+import ref_paged as ref
+from hierarchical_chunk_sparse_scoring_b200 import binding as hb
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def dense_table(lens, page):
+    """A table of consecutive pages for rows of these lengths, and the pages in use."""
+    need = [-(-n // page) for n in lens]
+    M = max(need) + 1
+    at, rows = 0, []
+    for c in need:
+        rows.append(list(range(at, at + c)) + [-1] * (M - c))
+        at += c
+    return ints(rows), at
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 1), (16, 1)])
+@pytest.mark.parametrize("n", [1, 2, 50, 4000])
+def test_attn_infinite_values_that_are_seen(n, Hq, Hkv, dtype):
+    """An infinite value reaches the output as itself: a positive weight times it."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    d, page = 64, 16
+    table, P = dense_table([n], page)
+    K, V = [torch.randn((P, Hkv, page, d), generator=g, device="cuda").to(dtype) for _ in range(2)]
+    q = torch.randn((1, Hq, d), generator=g, device="cuda").to(dtype)
+    if n == 50:
+        K.zero_()     # equal weights, exactly one
+    want, wlse = hb.paged_attn(q, K, V, table, ints([n - 1]))
+    for j, i, v in ((n - 1, 3, math.inf), (0, 5, -math.inf), (n // 2, 63, math.inf)):
+        V[j // page, :, j % page, i] = v
+    out, lse = hb.paged_attn(q, K, V, table, ints([n - 1]))
+    assert bool((out[..., 3] == math.inf).all()) and bool((out[..., 63] == math.inf).all())
+    assert bool((out[..., 5] == -math.inf).all())
+    rest = [i for i in range(d) if i not in (3, 5, 63)]
+    assert torch.equal(out[..., rest], want[..., rest]) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("Hq", [1, 4, 16])
+def test_attn_weights_keep_32_bits(Hq):
+    """Three tokens with values 0, 1 and -1 and logits 0, -x and -x - e: out is a difference of two
+    weights that agree in sixteen bits.  u = 2^-24: a logit is exact but for its factor (2 u x, x
+    below 0.7), a weight within 2 u more, the sums of products within 12 u, and the division by
+    more than two halves that: 8 u."""
+    d, page, T, e = 64, 8, 64, 2.0 ** -16
+    xs = 0.125 + torch.arange(1, T + 1, dtype=torch.float64) / 128     # (exact in bf16)
+    K = torch.zeros((T, 1, page, d), device="cuda")
+    V = torch.zeros((T, 1, page, d), device="cuda")
+    K[:, 0, 1:3, 0] = -xs.float().cuda()[:, None]
+    K[:, 0, 2, 1] = -e
+    V[:, 0, 1], V[:, 0, 2] = 1.0, -1.0
+    q = torch.zeros((T, Hq, d), device="cuda")
+    q[..., :2] = 1.0
+    out, _ = hb.paged_attn(q.to(BF), K.to(BF), V.to(BF), ints([[t] for t in range(T)]),
+                           ints([2] * T), scale=1.0)
+    a, b = torch.exp(-xs), torch.exp(-xs - e)
+    want = ((a - b) / (1 + a + b))[:, None, None].expand(T, Hq, d)
+    ref.within(out, want, torch.full_like(want, 8 * ref.U), BF)
