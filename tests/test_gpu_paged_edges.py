@@ -70,3 +70,28 @@ def test_attn_weights_keep_32_bits(Hq):
     a, b = torch.exp(-xs), torch.exp(-xs - e)
     want = ((a - b) / (1 + a + b))[:, None, None].expand(T, Hq, d)
     ref.within(out, want, torch.full_like(want, 8 * ref.U), BF)
+
+
+def test_attn_sums_of_long_rows_have_no_bias():
+    """Rows of 65536 tokens, thousands of tiles a warp: sums that are cut off and not rounded to
+    nearest would lean to one side with their length.  The values are positive and vary over many
+    steps of bf16, so the outputs' own roundings (half a step of 2^-7 at most, 2^-8 / sqrt(3)
+    each on average) fall evenly: their mean over N outputs is within 6 2^-8 / sqrt(3 N).  What
+    32 bits leave is a few u in each tile and 8 u sqrt(tiles) in rounded sums."""
+    T, Hq, d, n, page = 512, 8, 128, 65536, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    K, V = [torch.randn((n // page, 1, page, d), generator=g, device="cuda") for _ in range(2)]
+    K, V = K.to(BF), (0.5 + V.abs()).to(BF)
+    q = (3 * torch.randn((T, Hq, d), generator=g, device="cuda")).to(BF)
+    table = torch.arange(n // page, device="cuda", dtype=torch.int32)[None]
+    out, lse = hb.paged_attn(q, K, V, table, ints([n - 1] * T), seq=ints([0] * T))
+    off, worst = 0.0, 0.0
+    for t in range(0, T, 64):
+        x = q[t:t + 64].double().flatten(0, 1) @ K.double().reshape(n, d).T / math.sqrt(d)
+        z = torch.logsumexp(x, -1)
+        o = torch.exp(x - z[:, None]) @ V.double().reshape(n, d)
+        off += float((out[t:t + 64].double().flatten(0, 1) / o - 1).sum())
+        worst = max(worst, float((lse[t:t + 64].double().flatten() - z).abs().max()))
+    N = T * Hq * d
+    print("mean of the relative differences", off / N, "of the lse at most", worst)
+    assert abs(off / N) <= 6 * 2.0 ** -8 / math.sqrt(3 * N) + 8 * ref.U * math.sqrt(n / 16)
