@@ -190,7 +190,7 @@ extern "C" hils_status hils_qk_norm_rope(const hils_qk_params* p, const hils_rop
 
 extern "C" size_t hils_qk_backward_workspace_size(const hils_qk_params* p) {
   if (!p || p->d < 1 || p->d > kQkMaxD || p->d % 8 != 0) return 0;
-  return align_up((size_t)kQkBwdBlocks * 2 * (size_t)p->d * sizeof(float));
+  return align_up((size_t)kQkBwdBlocks * 2 * (size_t)p->d * sizeof(double));
 }
 
 extern "C" hils_status hils_qk_norm_rope_backward(
@@ -231,7 +231,7 @@ extern "C" hils_status hils_qk_norm_rope_backward(
   copy3(a.gks, p->ko_str);
   copy3(a.qos, p->dq_str);
   copy3(a.kos, p->dk_str);
-  a.dw_part = dw ? static_cast<float*>(workspace) : nullptr;
+  a.dw_part = dw ? static_cast<double*>(workspace) : nullptr;
   return done(launch_qk_norm_rope_bwd(a, p->dtype == HILS_BF16, p->grad_dtype == HILS_BF16, dw_q,
                                       dw_k, reinterpret_cast<cudaStream_t>(stream)));
 }

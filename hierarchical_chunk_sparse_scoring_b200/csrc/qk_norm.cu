@@ -333,14 +333,16 @@ __global__ void __launch_bounds__(kQkThreads, kQkBlocks)
 
 // ---------------------------------------------------------------------------------- backward
 
-// Gradients of the heads h0, h0 + hs, ... < H of one token; dw gains their share of this lane's
-// eight weight gradients.
+// Gradients of the heads h0, h0 + hs, ... < H of one token.  `sum` (shared memory, element i at
+// i LPR; null: no weight) gains their share of this lane's eight weight gradients: a token's heads
+// are added in 32 bits, tokens in 64, so that the error does not grow with their number.
 template <typename T, typename GT, int LPR, bool IL>
 __device__ __forceinline__ void grad_rows(const QkArgs& a, const LaneTurn& L, bool act,
                                           const T* src, int64_t sh, const GT* dy, int64_t gh,
                                           GT* dst, int64_t dh, int H, int h0, int hs,
-                                          const f2 (&w)[4], f2 (&dw)[4]) {
+                                          const f2 (&w)[4], double* sum) {
   constexpr int R = kBwdRows;
+  f2 dw[4] = {0ull, 0ull, 0ull, 0ull};
   const float inv_d = 1.f / (float)a.d;
   const bool actx = act && a.norm;
   Raw8<T> x[R];
@@ -387,6 +389,14 @@ __device__ __forceinline__ void grad_rows(const QkArgs& a, const LaneTurn& L, bo
       g[u] = gn[u];
     }
   }
+  if (sum) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = unpack2(dw[i]);
+      sum[2 * i * LPR] += t.x;
+      sum[(2 * i + 1) * LPR] += t.y;
+    }
+  }
 }
 
 // Blocks walk the token groups; each leaves its lanes' shares of the weight gradients, added over
@@ -395,17 +405,19 @@ template <typename T, typename GT, int LPR, bool IL>
 __global__ void __launch_bounds__(kQkThreads, kBwdBlocks)
     qk_norm_rope_bwd_kernel(const __grid_constant__ QkArgs a, int tbl) {
   constexpr int NLG = kQkThreads / LPR;
-  __shared__ float sDw[NLG][2][LPR * 8];
+  __shared__ double sDw[NLG][2][LPR * 8];   // element i of lane p at i LPR + p
   const int lg = threadIdx.x / LPR, p = threadIdx.x % LPR;
   const int h0 = lg >> tbl, hs = NLG >> tbl;
   const bool in_row = 8 * p < a.d;
   LaneTurn L;
   L.place(a.rope, p);
-  f2 wq[4], wk[4], dwq[4], dwk[4];
+  f2 wq[4], wk[4];
   load_weights<T>(a.wq, L, in_row, wq);
   load_weights<T>(a.wk, L, in_row, wk);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = 0ull;
+  for (int i = 0; i < 8; ++i) sDw[lg][0][i * LPR + p] = sDw[lg][1][i * LPR + p] = 0.0;
+  double* const sum_q = a.dw_part ? &sDw[lg][0][p] : nullptr;
+  double* const sum_k = a.dw_part ? &sDw[lg][1][p] : nullptr;
   for (int64_t t0 = (int64_t)blockIdx.x << tbl; t0 < a.tokens; t0 += (int64_t)gridDim.x << tbl) {
     const int64_t t = t0 + (lg & ((1 << tbl) - 1));
     const bool live = t < a.tokens, act = live && in_row;
@@ -414,51 +426,47 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocks)
     grad_rows<T, GT, LPR, IL>(a, L, act, static_cast<const T*>(a.q) + token_offset(a, a.qs, tt),
                           a.qs[1], static_cast<const GT*>(a.gq) + token_offset(a, a.gqs, tt),
                           a.gqs[1], static_cast<GT*>(a.qo) + token_offset(a, a.qos, tt),
-                          a.qos[1], a.Hq, h0, hs, wq, dwq);
+                          a.qos[1], a.Hq, h0, hs, wq, sum_q);
     grad_rows<T, GT, LPR, IL>(a, L, act, static_cast<const T*>(a.k) + token_offset(a, a.ks, tt),
                           a.ks[1], static_cast<const GT*>(a.gk) + token_offset(a, a.gks, tt),
                           a.gks[1], static_cast<GT*>(a.ko) + token_offset(a, a.kos, tt),
-                          a.kos[1], a.Hkv, h0, hs, wk, dwk);
+                          a.kos[1], a.Hkv, h0, hs, wk, sum_k);
   }
   if (!a.dw_part) return;
-  if (in_row) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = (i < 2 ? L.e0 : L.e1) + 2 * (i & 1);
-      const float2 u = unpack2(dwq[i]), v = unpack2(dwk[i]);
-      sDw[lg][0][e] = u.x;
-      sDw[lg][0][e + 1] = u.y;
-      sDw[lg][1][e] = v.x;
-      sDw[lg][1][e + 1] = v.y;
-    }
-  }
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * a.d; e += kQkThreads) {
-    const int which = e / a.d, i = e - which * a.d;
-    float v = 0.f;
+  for (int x = threadIdx.x; x < 2 * LPR * 8; x += kQkThreads) {
+    const int which = x / (LPR * 8), i = x / LPR % 8, lane = x % LPR;
+    if (8 * lane >= a.d) continue;
+    double v = 0.0;
 #pragma unroll
-    for (int g = 0; g < NLG; ++g) v += sDw[g][which][i];
-    a.dw_part[(int64_t)blockIdx.x * 2 * a.d + e] = v;
+    for (int g = 0; g < NLG; ++g) v += sDw[g][which][x % (LPR * 8)];
+    LaneTurn P;
+    P.place(a.rope, lane);
+    const int e = (i < 4 ? P.e0 : P.e1) + i % 4;
+    a.dw_part[((int64_t)blockIdx.x * 2 + which) * a.d + e] = v;
   }
 }
 
-// dw[e] = sum of the blocks' partials in a fixed order; 32 columns x 32 slices per block.
+// dw[e] = sum of the blocks' partials in a fixed order, rounded once; 32 columns x 32 slices per
+// block.
 __global__ void __launch_bounds__(1024)
-    qk_dw_join_kernel(const float* __restrict__ part, int blocks, int d, float* __restrict__ dw_q,
+    qk_dw_join_kernel(const double* __restrict__ part, int blocks, int d, float* __restrict__ dw_q,
                       float* __restrict__ dw_k) {
-  __shared__ float s[32][33];
+  __shared__ double s[32][33];
   const int c = threadIdx.x & 31, sl = threadIdx.x >> 5;
   const int e = blockIdx.x * 32 + c;
-  float v = 0.f;
+  double v = 0.0;
   if (e < 2 * d)
     for (int b = sl; b < blocks; b += 32) v += part[(int64_t)b * 2 * d + e];
   s[sl][c] = v;
   __syncthreads();
-  v = warp_sum(s[c][sl]);   // column sl of the block, over the 32 slices
+  v = s[c][sl];   // column sl of the block, over the 32 slices
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int o = blockIdx.x * 32 + sl;
   if (c == 0 && o < 2 * d) {
     float* dst = o < d ? dw_q : dw_k;
-    if (dst) dst[o < d ? o : o - d] = v;
+    if (dst) dst[o < d ? o : o - d] = (float)v;
   }
 }
 

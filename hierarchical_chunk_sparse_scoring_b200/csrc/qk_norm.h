@@ -31,7 +31,7 @@ struct QkArgs {
   int32_t Hq, Hkv, d, page_size, norm;
   float eps;
   int32_t* status;
-  float* dw_part;              // backward: [blocks][2][d]
+  double* dw_part;             // backward: [blocks][2][d]
   RopeTable rope;
 };
 

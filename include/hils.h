@@ -299,9 +299,9 @@ hils_status hils_qk_norm_rope(const hils_qk_params* p, const hils_rope* rope, co
  * and dk_out (qo_str, ko_str) and dq, dk (dq_str, dk_str) in grad_dtype, fp32 as hils_backward
  * returns them or dtype; dq may be dq_out and dk may be dk_out (same strides).  dw_q, dw_k fp32,
  * overwritten (zero when there are no rows), NULL to skip.  norm = 0: dx = g, no dw.  The weight
- * sums are formed per block and joined in a fixed order (no atomics): the same call on the same
- * device repeats bit for bit.  Workspace: hils_qk_backward_workspace_size bytes, 16-byte
- * aligned, no initialisation needed.
+ * sums (a token's heads in fp32, tokens in fp64, one rounding) are formed per block and joined in a
+ * fixed order (no atomics): the same call on the same device repeats bit for bit.  Workspace:
+ * hils_qk_backward_workspace_size bytes, 16-byte aligned, no initialisation needed.
  */
 size_t hils_qk_backward_workspace_size(const hils_qk_params* p);
 hils_status hils_qk_norm_rope_backward(const hils_qk_params* p, const hils_rope* rope,
