@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBlocks)
   const int64_t t = ((int64_t)blockIdx.x << tbl) + (lg & ((1 << tbl) - 1));
   const int h0 = lg >> tbl, hs = NLG >> tbl;
   bool live = t < a.tokens;
-  int64_t slot = 0;
+  int64_t slot = -1;
   if constexpr (PAGED) {
     if (live) slot = a.slot[t];
     if (slot >= a.n_slots) {

@@ -95,3 +95,16 @@ def test_attn_sums_of_long_rows_have_no_bias():
     N = T * Hq * d
     print("mean of the relative differences", off / N, "of the lse at most", worst)
     assert abs(off / N) <= 6 * 2.0 ** -8 / math.sqrt(3 * N) + 8 * ref.U * math.sqrt(n / 16)
+
+
+def test_append_to_an_empty_pool():
+    """Padding asks for nothing, so nothing is recorded; a slot that no pool holds is."""
+    T, d = 593, 64
+    q, k, v = [torch.randn((T, h, d), device="cuda") for h in (2, 1, 1)]
+    K = torch.empty((0, 1, 16, d), device="cuda")
+    ws = hb.paged_workspace(device="cuda")
+    for slots, status in (([-1] * T, 0), ([-1] * (T - 1) + [0], 5)):
+        out = torch.full((T, 2, d), 7.0, device="cuda")
+        hb.paged_append(q, k, v, None, None, hb.rope(64), K, K.clone(), ints([0] * T), ints(slots),
+                        q_out=out, ws=ws)
+        assert hb.device_status(ws) == status and bool((out == 7).all())
