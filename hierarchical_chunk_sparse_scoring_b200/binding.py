@@ -674,14 +674,43 @@ def paged_workspace(q=None, K=None, *, device=None, stream=None):
     return _run(device, stream, (), go)
 
 
-def _workspace_of(ws, device, n):
-    """The caller's workspace, or one for this call (its status word zeroed)."""
-    if ws is None:
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+# workspaces of the paged calls made without one: (device index, stream handle) -> workspace
+_paged_ws = {}
+
+
+def _workspace_of(ws, device, n, st):
+    """The caller's workspace, or the one kept for such calls on this device and stream `st`."""
+    if ws is not None:
+        if ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+            _refuse(ws, "ws", torch.uint8, ws.shape, device)
+        return ws
+    n = max(n, 256)
+    if torch.cuda.is_current_stream_capturing():   # a graph may run beside this stream's calls
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
         ws[:256].zero_()
-    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        _refuse(ws, "ws", torch.uint8, ws.shape, device)
+        return ws
+    ws = _paged_ws.get((device.index, st))
+    if ws is None or ws.numel() < n:
+        new = torch.empty(n, dtype=torch.uint8, device=device)
+        if ws is None:
+            _check(lib().hils_workspace_init(_addr(new), n, st), "hils_workspace_init")
+        else:
+            new[:256].copy_(ws[:256])              # what is recorded so far
+        _paged_ws[device.index, st] = ws = new
     return ws
+
+
+def paged_status(stream=None):
+    """Reads and clears what the paged calls made without `ws` on this stream (default: the current
+    one of the current device) recorded: 0, or 5 if a length, page, slot or position was refused.
+    A call captured in a graph without `ws` has a workspace that nothing reads: give it one."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    ws = _paged_ws.get((stream.device.index, stream.cuda_stream))
+    if ws is None:
+        return 0
+    with torch.cuda.device(stream.device):
+        return device_status(ws, stream)
 
 
 def paged_plan(kv_len, new_len, block_table, free_pages, n_free, *, page_size, T_cap,
@@ -690,7 +719,8 @@ def paged_plan(kv_len, new_len, block_table, free_pages, n_free, *, page_size, T
     they need taken from the free stack (free_pages [n_pages], n_free [1]) and entered in
     block_table [B,max_pages] (in place).  T_cap bounds the tokens.  kv_len_out and n_free_out may
     be kv_len and n_free.  Returns a dict: slot, pos, seq [T_cap], cu [B+1], kv_len [B],
-    n_free [1], all int32."""
+    n_free [1], all int32.  Refused sequences and bad pages are recorded in ws (device_status), or,
+    without it, for paged_status."""
     B, M = block_table.shape
     P = free_pages.numel()
     dev = block_table.device
@@ -716,7 +746,7 @@ def paged_plan(kv_len, new_len, block_table, free_pages, n_free, *, page_size, T
             kv = kv_len_out
         if n_free_out is not None:
             nf = n_free_out
-        w = _workspace_of(ws, dev, 256)
+        w = _workspace_of(ws, dev, 256, st)
         p = _PAGED.pack(T_cap, B, 0, 0, 0, P, M, 0, 0, 0, page_size, 0, 0, 0.0)
         _check(lib().hils_paged_plan(p, _addr(kv_len), _addr(new_len), _addr(block_table),
                                      _addr(free_pages), _addr(n_free), _addr(kv), _addr(nf),
@@ -733,7 +763,8 @@ def paged_append(q, k, v, w_q, w_k, rope, K, V, pos, slot, *, eps=1e-6, norm=Tru
     """hils_paged_append: qk_norm_rope of a step's tokens q [T,Hq,d], k, v [T,Hkv,d] (any strides)
     at pos [T], keys and values written to slot [T] of the pools K, V [n_pages,Hkv,page_size,d]
     (any strides; a [n_pages,page_size,Hkv,d] pool as its transpose).  Returns q_out, whose
-    padding rows (slot < 0) are left as they were (zero where it is allocated here)."""
+    padding rows (slot < 0) are left as they were (zero where it is allocated here).  Slots past
+    the pool are recorded in ws (device_status), or, without it, for paged_status."""
     if not q.is_cuda:
         raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
     T, Hq, d = q.shape
@@ -755,7 +786,7 @@ def paged_append(q, k, v, w_q, w_k, rope, K, V, pos, slot, *, eps=1e-6, norm=Tru
         out = torch.zeros_like(q, memory_format=torch.contiguous_format) if q_out is None \
             else q_out
         so = _out_rows(out, "q_out", dt, (T, Hq, d), dev)
-        w = _workspace_of(ws, dev, 256)
+        w = _workspace_of(ws, dev, 256, st)
         code = _dtype_code(dt)
         p = _QK.pack(1, T, Hq, Hkv, d, 0, 0, sq[1], sq[0], 0, sk[1], sk[0], 0, sv[1], sv[0], 0,
                      so[1], so[0], 0, 0, 0, 0, 0, 0, 0, 0, 0, code, code, int(bool(norm)), eps)
@@ -774,7 +805,9 @@ def paged_attn(q, K, V, block_table, pos, *, seq=None, window=0, scale=0.0, out=
     """hils_paged_attn: row t of q [T,Hq,d] attends to tokens 0 .. pos[t] (the last `window` of
     them, if given) of sequence seq[t] (default t) in the pools K, V [n_pages,Hkv,page_size,d]
     (any strides) through block_table [B,max_pages].  Returns (out [T,Hq,d], lse [T,Hq] fp32);
-    padding rows (seq < 0) are left as they were (zero where `out` is allocated here)."""
+    padding rows (seq < 0) are left as they were (zero where `out` is allocated here).  Bad
+    positions, sequences and pages are recorded in ws (device_status), or, without it, for
+    paged_status."""
     if not q.is_cuda:
         raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
     T, Hq, d = q.shape
@@ -802,7 +835,7 @@ def paged_attn(q, K, V, block_table, pos, *, seq=None, window=0, scale=0.0, out=
             z = q.new_empty((T, Hq), dtype=torch.float32) if seq is None else \
                 q.new_zeros((T, Hq), dtype=torch.float32)
         c = _PAGED.pack(T, B, Hq, Hkv, d, P, M, *sc[:3], ps, window, _dtype_code(dt), scale)
-        w = _workspace_of(ws, dev, 0 if ws is not None else lib().hils_paged_workspace_size(c))
+        w = _workspace_of(ws, dev, 0 if ws is not None else lib().hils_paged_workspace_size(c), st)
         _check(lib().hils_paged_attn(c, _addr(q), _addr(K), _addr(V), _addr(block_table),
                                      _addr(seq), _addr(pos), _addr(o), _addr(z), _addr(w),
                                      w.numel(), st), "hils_paged_attn")

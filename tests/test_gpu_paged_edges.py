@@ -108,3 +108,51 @@ def test_append_to_an_empty_pool():
         hb.paged_append(q, k, v, None, None, hb.rope(64), K, K.clone(), ints([0] * T), ints(slots),
                         q_out=out, ws=ws)
         assert hb.device_status(ws) == status and bool((out == 7).all())
+
+
+def test_calls_without_a_workspace_record_where_it_can_be_read():
+    hb.paged_status()
+    d, page = 64, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    K, V = [torch.randn((4, 1, page, d), generator=g, device="cuda") for _ in range(2)]
+    q = torch.randn((2, 2, d), generator=g, device="cuda")
+    good, pos = ints([[0, 1], [2, 3]]), ints([20, 30])
+
+    def plan(new):
+        return hb.paged_plan(ints([5]), ints([new]), ints([[0, -1]]), ints([3, 2, 1, 0]), ints([2]),
+                             page_size=page, T_cap=64)
+
+    def append(slot):
+        return hb.paged_append(q, q[:, :1], q[:, :1], None, None, hb.rope(d), K, V, pos, ints(slot))
+
+    def attn(table, rows=q):
+        return hb.paged_attn(rows, K, V, table, pos)
+
+    for ok, bad in ((lambda: plan(3), lambda: plan(40)),
+                    (lambda: append([-1, 3]), lambda: append([3, 64])),
+                    (lambda: attn(good), lambda: attn(ints([[0, 4], [2, 3]])))):
+        ok()
+        assert hb.paged_status() == 0
+        bad()
+        ok()
+        assert hb.paged_status() == 5 and hb.paged_status() == 0
+    # the word survives a workspace that has to grow, and belongs to its stream
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    append([64, 64])
+    wide = torch.randn((2, 16, d), generator=g, device="cuda")
+    attn(good, wide)
+    hb.paged_attn(q, K, V, good, pos, stream=side)
+    assert hb.paged_status(side) == 0 and hb.paged_status() == 5
+    # a captured call has a workspace of its own
+    want = attn(good)
+    p = pos.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = hb.paged_attn(q, K, V, good, p)
+    p.fill_(1 << 20)
+    graph.replay()
+    assert hb.paged_status() == 0
+    p.copy_(pos)
+    graph.replay()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
