@@ -112,6 +112,25 @@ bool attn_shape_ok(const hils_paged_params* c) {
          paged_attn_supported(c->d, c->Hq / c->Hkv);
 }
 
+// Whether two tensors share their first element, unless with the same strides (in the dimensions
+// [B, H, N] of more than one entry) and element sizes, as an operator in place has them.
+bool clash(const void* x, const int64_t (&xs)[3], int64_t ex, const void* y,
+           const int64_t (&ys)[3], int64_t ey, int64_t B, int64_t H, int64_t N) {
+  if (!x || x != y) return false;
+  return ex != ey || (B > 1 && xs[0] != ys[0]) || (H > 1 && xs[1] != ys[1]) ||
+         (N > 1 && xs[2] != ys[2]);
+}
+
+// A contiguous int32 array of a call.
+struct Ints {
+  const int32_t* p;
+  int64_t n;
+  bool overlaps(const Ints& o) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+    return n > 0 && o.n > 0 && a < b + 4 * (uint64_t)o.n && b < a + 4 * (uint64_t)n;
+  }
+};
+
 hils_status done(cudaError_t e) { return e == cudaSuccess ? HILS_OK : HILS_ERR_CUDA; }
 
 }  // namespace
@@ -179,6 +198,10 @@ extern "C" hils_status hils_qk_norm_rope(const hils_qk_params* p, const hils_rop
                 !ok_strides(p->ko_str, es, p->B, p->Hkv, p->N, p->d, true))))
     return HILS_ERR_INVALID_ARG;
   if (!anyq && !anyk) return HILS_OK;
+  if ((anyq && clash(q, p->q_str, es, q_out, p->qo_str, es, p->B, p->Hq, p->N)) ||
+      (anyk && clash(k, p->k_str, es, k_out, p->ko_str, es, p->B, p->Hkv, p->N)) ||
+      (anyq && anyk && (q_out == k || k_out == q || q_out == k_out)))
+    return HILS_ERR_INVALID_ARG;
   if ((s = check_device()) != HILS_OK) return s;
   QkArgs a = qk_args(p, rope);
   a.q = q; a.k = k; a.wq = w_q; a.wk = w_k; a.pos = pos; a.qo = q_out; a.ko = k_out;
@@ -221,6 +244,15 @@ extern "C" hils_status hils_qk_norm_rope_backward(
              workspace_bytes < hils_qk_backward_workspace_size(p)))
     return HILS_ERR_WORKSPACE;
   if (!anyq && !anyk && !dw) return HILS_OK;
+  // (without a norm q and k are not read)
+  const void *xq = p->norm ? q : nullptr, *xk = p->norm ? k : nullptr;
+  if ((anyq && (clash(dq_out, p->qo_str, gs, dq, p->dq_str, gs, p->B, p->Hq, p->N) ||
+                clash(xq, p->q_str, es, dq, p->dq_str, gs, p->B, p->Hq, p->N))) ||
+      (anyk && (clash(dk_out, p->ko_str, gs, dk, p->dk_str, gs, p->B, p->Hkv, p->N) ||
+                clash(xk, p->k_str, es, dk, p->dk_str, gs, p->B, p->Hkv, p->N))) ||
+      (anyq && anyk && (dq == dk || dq == dk_out || dk == dq_out || dq == xk || dk == xq)) ||
+      (dw && dw_q == dw_k))
+    return HILS_ERR_INVALID_ARG;
   if ((s = check_device()) != HILS_OK) return s;
   QkArgs a = qk_args(p, rope);
   if (!anyq) a.Hq = 0;
@@ -260,6 +292,16 @@ extern "C" hils_status hils_paged_plan(const hils_paged_params* p, const int32_t
     return HILS_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) || workspace_bytes < kStatusBytes)
     return HILS_ERR_WORKSPACE;
+  const Ints in[] = {{kv_len, p->B}, {n_free, 1}, {new_len, p->B}, {free_pages, p->n_pages}};
+  const Ints out[] = {{kv_len_out, p->B}, {n_free_out, 1}, {block_table, p->B * p->max_pages},
+                      {cu, p->B + 1},     {slot, p->T},    {pos, p->T}, {seq, p->T}};
+  for (int i = 0; i < 7; ++i) {
+    for (int j = 0; j < 4; ++j)   // (lengths and the free count may be updated in place)
+      if (out[i].overlaps(in[j]) && !(i == j && i < 2 && out[i].p == in[j].p))
+        return HILS_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[i].overlaps(out[j])) return HILS_ERR_INVALID_ARG;
+  }
   if ((s = check_device()) != HILS_OK) return s;
   PlanArgs a;
   a.B = (int32_t)p->B;
@@ -303,6 +345,9 @@ extern "C" hils_status hils_paged_append(const hils_qk_params* p, const hils_rop
   if (!workspace || !aligned16(workspace) || workspace_bytes < kStatusBytes)
     return HILS_ERR_WORKSPACE;
   if (!anyq && !anyk) return HILS_OK;
+  if ((anyq && clash(q, p->q_str, es, q_out, p->qo_str, es, p->B, p->Hq, p->N)) ||
+      (anyq && anyk && (q_out == k || q_out == v)) || (pool && K == V))
+    return HILS_ERR_INVALID_ARG;
   if ((s = check_device()) != HILS_OK) return s;
   QkArgs a = qk_args(p, rope);
   a.q = q; a.k = k; a.v = v; a.wq = w_q; a.wk = w_k; a.pos = pos; a.slot = slot; a.qo = q_out;

@@ -271,10 +271,12 @@ hils_status hils_rope_init(hils_rope* rope, int32_t rot_dim, int32_t layout, int
  * q, q_out [B, Hq, N, d] and k, k_out [B, Hkv, N, d] by strides (elements; batch, head, token;
  * the head dim is contiguous), so heads-first and tokens-first tensors and slices of one fused
  * projection are read in place; every stride and base a multiple of 16 bytes.  Output rows must
- * not overlap; q_out may be q and k_out may be k (same strides).  w_q, w_k [d] in dtype, NULL for
- * ones.  norm = 0: rotation only (w_q, w_k NULL).  pos [B, N] int32, or NULL for pos0 + n.
- * Hq or Hkv may be 0.  d a multiple of 8 up to 256.  Sums, statistics and products are fp32, one
- * rounding to dtype at the end.  Allocates nothing, needs no workspace, asynchronous on `stream`.
+ * not overlap; q_out may be q and k_out may be k (same strides), and no other tensor of the call may
+ * lie under an output (tensors that start at one address in any other way are refused).  w_q, w_k
+ * [d] in dtype, NULL for ones.  norm = 0: rotation only (w_q, w_k NULL).  pos [B, N] int32, or NULL
+ * for pos0 + n.  Hq or Hkv may be 0.  d a multiple of 8 up to 256.  Sums, statistics and products
+ * are fp32, one rounding to dtype at the end.  Allocates nothing, needs no workspace, asynchronous
+ * on `stream`.
  */
 typedef struct {
   int64_t B, N, Hq, Hkv, d;
@@ -297,10 +299,11 @@ hils_status hils_qk_norm_rope(const hils_qk_params* p, const hils_rope* rope, co
  * Its gradients.  With g = R_p^T dy:  dw = sum over rows of g * x r (fp32, [d]),
  * dx = r (w g - x r^2 mean(w g x)).  q, k, w_q, w_k, pos as given to hils_qk_norm_rope; dq_out
  * and dk_out (qo_str, ko_str) and dq, dk (dq_str, dk_str) in grad_dtype, fp32 as hils_backward
- * returns them or dtype; dq may be dq_out and dk may be dk_out (same strides).  dw_q, dw_k fp32,
- * overwritten (zero when there are no rows), NULL to skip.  norm = 0: dx = g, no dw.  The weight
- * sums (a token's heads in fp32, tokens in fp64, one rounding) are formed per block and joined in a
- * fixed order (no atomics): the same call on the same device repeats bit for bit.  Workspace:
+ * returns them or dtype; dq may be dq_out and dk may be dk_out (same strides), no other tensor may
+ * lie under an output (refused where they start at one address).  dw_q, dw_k fp32, overwritten
+ * (zero when there are no rows), NULL to skip.  norm = 0: dx = g, no dw.  The weight sums (a
+ * token's heads in fp32, tokens in fp64, one rounding) are formed per block and joined in a fixed
+ * order (no atomics): the same call on the same device repeats bit for bit.  Workspace:
  * hils_qk_backward_workspace_size bytes, 16-byte aligned, no initialisation needed.
  */
 size_t hils_qk_backward_workspace_size(const hils_qk_params* p);
@@ -345,11 +348,12 @@ size_t hils_paged_workspace_size(const hils_paged_params* p);
  * numbered in order of (b, position), token t < cu[B]:  seq[t] = b, pos[t] = its position,
  * slot[t] = its slot; tokens cu[B] .. T - 1 get -1 in all three.  cu [B + 1] counts the tokens
  * before each sequence; kv_len_out = kv_len + new_len and n_free_out the pages left, each may be
- * its input (in place); no other arrays of the call may overlap.  A sequence is refused (no tokens, no pages, length kept, recorded in the
- * status word) if a length is negative, if it would outgrow max_pages, or if the tokens or pages
- * asked for up to and including it exceed T or the free pages (one that needs no new page is not
- * refused for pages).  A page id outside the pool gives slot -1 and is recorded.  Reads T, B,
- * n_pages, max_pages, page_size of `p`; B <= 8192, T < 2^31.  Workspace: 256 bytes.
+ * its input (in place); a call with any other output under another array is refused.  A sequence is
+ * refused (no tokens, no pages, length kept, recorded in the status word) if a length is negative,
+ * if it would outgrow max_pages, or if the tokens or pages asked for up to and including it exceed
+ * T or the free pages (one that needs no new page is not refused for pages).  A page id outside the
+ * pool gives slot -1 and is recorded.  Reads T, B, n_pages, max_pages, page_size of `p`; B <= 8192,
+ * T < 2^31.  Workspace: 256 bytes.
  */
 hils_status hils_paged_plan(const hils_paged_params* p, const int32_t* kv_len,
                             const int32_t* new_len, int32_t* block_table,
@@ -363,8 +367,9 @@ hils_status hils_paged_plan(const hils_paged_params* p, const int32_t* kv_len,
  * their slots of the cache: token t (B = 1, N = T of `p`; v by v_str) turns at pos[t]; its query
  * goes to q_out row t, its key and value to slot[t].  A token with a negative slot is padding:
  * nothing of it is written, its q_out row is left as it was.  So is one with a slot beyond the
- * pool, which is recorded.  The slots of a call must be distinct.  `c` gives the cache (n_pages,
- * page_size, c_str; T, Hq, Hkv, d and dtype as in `p`).  Workspace: 256 bytes.
+ * pool, which is recorded.  The slots of a call must be distinct, K and V different pools.  `c`
+ * gives the cache (n_pages, page_size, c_str; T, Hq, Hkv, d and dtype as in `p`).  Workspace: 256
+ * bytes.
  */
 hils_status hils_paged_append(const hils_qk_params* p, const hils_rope* rope,
                               const hils_paged_params* c, const void* q, const void* k,
@@ -382,10 +387,11 @@ hils_status hils_paged_append(const hils_qk_params* p, const hils_rope* rope,
  * or seq[t] >= B, which is recorded; tokens in a page outside the pool count as unseen and are
  * recorded.  A row with seq[t] < 0 is padding, left as it was.  The work is split evenly over the
  * SMs along the rows' lengths and joined in a fixed order, so a call repeats bit for bit (where a
- * row is split, and with it its last bits, depends on the other rows' lengths); the launches do not depend on the lengths, so a step can be captured in a CUDA graph.  Supported:
- * d = 64 or 128, G = Hq / Hkv <= 16.  bf16: products on the tensor cores, softmax weights carried
- * as three bf16 (all of their 24 bits) for the product with V, sums fp32; fp32: all fp32.  An
- * infinite value that a row sees with a weight of at least 2^-96 of its largest is in its output.  A row whose every
+ * row is split, and with it its last bits, depends on the other rows' lengths); the launches do not
+ * depend on the lengths, so a step can be captured in a CUDA graph.  Supported: d = 64 or 128,
+ * G = Hq / Hkv <= 16.  bf16: products on the tensor cores, softmax weights carried as three bf16
+ * (all of their 24 bits) for the product with V, sums fp32; fp32: all fp32.  An infinite value that
+ * a row sees with a weight of at least 2^-96 of its largest is in its output.  A row whose every
  * logit is -inf gives out 0, lse -inf.
  */
 hils_status hils_paged_attn(const hils_paged_params* p, const void* q, const void* K,
