@@ -156,3 +156,123 @@ def test_calls_without_a_workspace_record_where_it_can_be_read():
     p.copy_(pos)
     graph.replay()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def split_places(lens, Hkv, kt):
+    """Places of the split's list for rows of these lengths: a unit of n tiles takes n + 1."""
+    return sum(-(-n // kt) + 1 for n in lens if n) * Hkv
+
+
+def check_every_tile(lens, Hq, Hkv, dtype, d=64, window=0):
+    """With q = 0 every weight is one and lse = ln n; V is one-hot in the group of eight tokens, so
+    each group adds one eighth of a tile's count to a dimension of its own (groups 8 d tokens apart
+    share one).  Weights, factors and sums are whole numbers below 2^24, exact in 32 bits, so an
+    output is a count over n within the division (3 u) and its rounding, and the logarithm within
+    4 u of its value."""
+    page = 64
+    table, P = dense_table(lens, page)
+    V = torch.zeros((P, Hkv, page, d), device="cuda", dtype=dtype)
+    at = 0
+    dims = torch.arange(max(max(lens), 1), device="cuda") // 8 % d
+    for n in lens:
+        j = torch.arange(n, device="cuda")
+        V[at + j // page, :, j % page, dims[:n]] = 1.0
+        at += -(-n // page)
+    K = torch.zeros_like(V)
+    q = torch.zeros((len(lens), Hq, d), device="cuda", dtype=dtype)
+    out, lse = hb.paged_attn(q, K, V, table, ints([n - 1 for n in lens]), window=window)
+    lo = [max(0, n - window) if window else 0 for n in lens]
+    count = torch.zeros((len(lens), d), dtype=torch.float64, device="cuda")
+    for t, n in enumerate(lens):
+        count[t] = torch.bincount(dims[lo[t]:n], minlength=d)[:d]
+    size = torch.tensor([float(n - a) for n, a in zip(lens, lo)], dtype=torch.float64,
+                        device="cuda")
+    want = torch.where(size[:, None] > 0, count / size.clamp(min=1)[:, None], 0.0)
+    got = out.double()
+    half = ref.HALF_STEP[dtype]
+    assert bool(((got - want[:, None]).abs() <= (half + 3 * ref.U) * want[:, None]).all()), lens
+    wl = torch.log(size)
+    ok = (lse.double() == wl[:, None]) | ((lse.double() - wl[:, None]).abs() <=
+                                          4 * ref.U * (wl[:, None].abs() + 1))
+    assert bool(ok.all()), lens
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("lens,Hq,Hkv", [
+    ([70001], 8, 1), ([70001], 1, 1), ([30011, 3, 50000], 16, 1), ([20000, 0, 0, 9999], 4, 4),
+    ([131072, 131071], 6, 2), ([1] * 500 + [60000] + [2] * 300, 2, 2)])
+def test_attn_every_tile_of_long_rows(lens, Hq, Hkv, dtype):
+    check_every_tile(lens, Hq, Hkv, dtype)
+    check_every_tile(lens, Hq, Hkv, dtype, d=128, window=17003)
+
+
+@pytest.mark.parametrize("dtype,kt", [(BF, 16), (F32, 8)], ids=["bf16", "fp32"])
+def test_attn_every_tile_at_every_cut(dtype, kt):
+    """A short row before a long one moves the long one's cuts place by place: over a whole stretch
+    of a block and then some, so that blocks and warps begin at a unit's own place, at its first
+    tile, behind it, and at the place after a whole stretch."""
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    base = kt * ctas * 20
+    per = split_places([base], 1, kt) // ctas + 1
+    seen = set()
+    for shift in range(0, per + 12):
+        lens = [shift * kt, base, 5 * kt]
+        step = max(4, int(split_places(lens, 1, kt) / ctas) + 1)
+        seen |= {((c * step) - split_places(lens[:1], 1, kt)) for c in range(ctas)
+                 if 0 <= c * step - split_places(lens[:1], 1, kt) <= step + 1}
+        check_every_tile(lens, 8, 1, dtype)
+    assert {0, 1, 2, per - 1, per, per + 1} <= seen
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (16, 1), (4, 4), (6, 2)])
+def test_attn_every_tile_of_random_batches(Hq, Hkv, dtype):
+    g = torch.Generator().manual_seed(Hq)
+    for i in range(40):
+        T = int(torch.randint(1, 200, (1,), generator=g))
+        top = int(2 ** (4 + 10 * float(torch.rand(1, generator=g))))
+        lens = torch.randint(0, top, (T,), generator=g).tolist()
+        lens[int(torch.randint(0, T, (1,), generator=g))] = 20 * top
+        check_every_tile(lens, Hq, Hkv, dtype, window=[0, 0, 3 * top // 2][i % 3])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("tokens", [131072, 160001, 400009])
+def test_plan_of_many_tokens(tokens, in_place):
+    """More tokens than the grid has threads, the last round not a whole one."""
+    B, page = 53, 16
+    g = torch.Generator().manual_seed(tokens)
+    kv = torch.randint(0, 3000, (B,), generator=g)
+    new = torch.full((B,), tokens // B)
+    new[7] += tokens - int(new.sum()) - 9
+    have, end = (kv + page - 1) // page, (kv + new + page - 1) // page
+    P, M = int(end.sum()) + 3, int(end.max()) + 1
+    perm = torch.randperm(P, generator=g)
+    first = have.cumsum(0) - have
+    col = torch.arange(M)[None]
+    table = torch.where(col < have[:, None], perm[(first[:, None] + col).clamp(max=P - 1)], -1)
+    n_free = P - int(have.sum())
+    free = torch.cat([perm[int(have.sum()):], torch.zeros(P - n_free, dtype=torch.long)])
+    # the pages a sequence takes come from the top of the stack in order of (sequence, page)
+    before = (end - have).cumsum(0) - (end - have)
+    fresh = (col >= have[:, None]) & (col < end[:, None])
+    want = torch.where(fresh, free[(n_free - 1 - (before[:, None] + col - have[:, None])).clamp(
+        0, P - 1)], table)
+    n = int(new.sum())
+    seq = torch.repeat_interleave(torch.arange(B), new)
+    cu = torch.cat([torch.zeros(1, dtype=torch.long), new.cumsum(0)])
+    pos = kv[seq] + torch.arange(n) - cu[seq]
+    tail = torch.full((tokens - n,), -1)
+    tab, kvt, nft = ints(table.tolist()), ints(kv.tolist()), ints([n_free])
+    kw = dict(kv_len_out=kvt, n_free_out=nft) if in_place else {}
+    ws = hb.paged_workspace(device="cuda")
+    got = hb.paged_plan(kvt, ints(new.tolist()), tab, ints(free.tolist()), nft, page_size=page,
+                        T_cap=tokens, ws=ws, **kw)
+    assert hb.device_status(ws) == 0
+    assert torch.equal(tab.cpu().long(), want)
+    slot = want[seq, pos // page] * page + pos % page
+    for name, w in (("seq", seq), ("pos", pos), ("slot", slot)):
+        assert torch.equal(got[name].cpu().long(), torch.cat([w, tail])), name
+    assert torch.equal(got["cu"].cpu().long(), cu)
+    assert torch.equal(got["kv_len"].cpu().long(), kv + new)
+    assert got["n_free"].tolist() == [n_free - int((end - have).sum())]
