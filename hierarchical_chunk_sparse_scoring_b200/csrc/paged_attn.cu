@@ -222,10 +222,11 @@ struct PaShape {
   static constexpr int HALF = KT * ROW;                     // K (or V) of a tile
   static constexpr int STAGE = 2 * HALF;
   // Warps, and the stages of each one's ring.  The first part of a warp (G D floats) waits in
-  // shared memory where that fits beside the rings, else in the workspace.  (bf16 of 16 heads: six
-  // warps with their parts in shared memory beat eight with them in the workspace, 32 rows of
-  // 16384 tokens 61 us against 66 us; fp32, bound by instructions, wants the eight.)
-  static constexpr int NW = GM > 8 && sizeof(T) == 2 ? 6 : 8;
+  // shared memory where that fits beside the rings, else in the workspace.  (bf16 of 16 heads: as
+  // many warps as fit with their parts.  32 rows of 16384 tokens, d = 128: 68 us with seven, 76 with
+  // six, 73 with eight and the parts in the workspace; d = 64: 49 us with eight, 52 with seven, 58
+  // with six.  fp32, bound by instructions, wants the eight.)
+  static constexpr int NW = GM > 8 && sizeof(T) == 2 && D > 64 ? 7 : 8;
   static constexpr int ST = 24576 / STAGE;
   static constexpr bool FIRST_SMEM = GM <= 4 || sizeof(T) == 2 || (GM <= 8 && D == 64);
   static constexpr int FIRST = FIRST_SMEM ? GM * D : 0;
@@ -315,7 +316,7 @@ struct PaWarp<__nv_bfloat16, D, GM> {
     const bool see0 = (mask >> (lane / 4)) & 1, see1 = (mask >> (lane / 4 + 8)) & 1;
     // The weights as three bf16 each, all 24 bits of them.  (One alone would add as much error as the
     // rounding of the output, two leave 16 bits.  Three cost nothing: 64 ragged rows 181 us with two
-    // or three, 32 rows of 16384 tokens and 16 heads 79 us either way, cold cache.)
+    // or three.)
     uint32_t p[NB][3][2];
     float f[NB][2];
 #pragma unroll
@@ -350,8 +351,8 @@ struct PaWarp<__nv_bfloat16, D, GM> {
     }
     // The tile's sums apart, smallest parts first, then added to O: the products cut their sums off
     // and do not round to nearest, which over thousands of tiles in one accumulator leaned the
-    // output towards zero by 2e-4 (rows of 65536 tokens).  (64 ragged rows 181 us either way; with
-    // 16 heads, 32 rows of 16384 tokens, cold cache: d = 128 79 us either way, d = 64 59 -> 66 us.)
+    // output towards zero by 2e-4 (rows of 65536 tokens).  (It costs nothing up to 8 heads of
+    // d = 128, 64 ragged rows 181 us either way, and 2% at d = 64, 64 rows of 16384 tokens.)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       uint32_t a[4];
