@@ -453,7 +453,9 @@ def rope(rot_dim, *, layout="half", scaling="plain", base=10000.0, factor=1.0, t
          beta_fast=32.0, beta_slow=1.0, freq=None, mscale=None):
     """The rotary position code of a model (hils_rope_init): pairs of the first rot_dim
     dimensions, "half" or "interleaved", under the scaling rule "plain", "linear", "ntk", "yarn"
-    or "hope".  `freq` (rot_dim / 2 radians per position) and `mscale` replace the rule's."""
+    or "hope".  `freq` (rot_dim / 2 radians per position) and `mscale` replace the rule's.  (The
+    ramp of "yarn" runs over the turns a pair makes in the trained length, as in the paper; a
+    checkpoint whose ramp runs over the pair's index needs its `freq`.)"""
     if layout not in _LAYOUTS or scaling not in _SCALINGS:
         raise ValueError("layout is one of %s, scaling one of %s" %
                          (sorted(_LAYOUTS), sorted(_SCALINGS)))
@@ -804,10 +806,10 @@ def paged_attn(q, K, V, block_table, pos, *, seq=None, window=0, scale=0.0, out=
                ws=None, stream=None):
     """hils_paged_attn: row t of q [T,Hq,d] attends to tokens 0 .. pos[t] (the last `window` of
     them, if given) of sequence seq[t] (default t) in the pools K, V [n_pages,Hkv,page_size,d]
-    (any strides) through block_table [B,max_pages].  Returns (out [T,Hq,d], lse [T,Hq] fp32);
-    padding rows (seq < 0) are left as they were (zero where `out` is allocated here).  Bad
-    positions, sequences and pages are recorded in ws (device_status), or, without it, for
-    paged_status."""
+    (any strides; d = 64 or 128, at most 16 heads per KV head) through block_table [B,max_pages].
+    Returns (out [T,Hq,d], lse [T,Hq] fp32); padding rows (seq < 0) are left as they were (zero
+    where `out` is allocated here).  Bad positions, sequences and pages are recorded in ws
+    (device_status), or, without it, for paged_status."""
     if not q.is_cuda:
         raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
     T, Hq, d = q.shape

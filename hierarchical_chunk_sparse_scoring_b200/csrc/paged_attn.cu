@@ -12,12 +12,13 @@
 // lengths; CTAs sum the rows' tiles themselves, so nothing about the lengths is needed on the
 // host.  (Short units are not cut; they go with their first place.)  A warp walks its stretch with
 // its own ring of cp.async stages, across unit boundaries, and its own running maximum and sum,
-// and writes units that lie within it: no block barrier until every warp is done.  Then the parts (m, sum, O) of units cut by a warp boundary are added
-// in shared memory, and those of units cut by a CTA boundary go to the workspace, where the join
-// kernel adds them, always in the list's order.  The 128 KB a CTA has in flight cover the
-// latency of HBM; a tile's page id is read one tile ahead of its copy.
-// Measured (bf16, 32/8 heads, d = 128): 8 rows of 120K tokens 573 us = 6.8 TB/s, 64 ragged rows of
-// 500 to 15K tokens 179 us = 6.2 TB/s; one row of 1000 tokens 10 us, a chain of latencies (the
+// and writes units that lie within it: no block barrier until every warp is done.  Then the parts
+// (m, sum, O) of units cut by a warp boundary are added in shared memory, and those of units cut by
+// a CTA boundary go to the workspace, where the join kernel adds them, always in the list's order.
+// The 128 KB a CTA has in flight cover the latency of HBM; a tile's page id is read one tile ahead
+// of its copy.
+// Measured (bf16, 32/8 heads, d = 128): 8 rows of 120K tokens 577 us = 6.7 TB/s, 64 ragged rows of
+// 500 to 15K tokens 183 us = 6.1 TB/s; one row of 1000 tokens 11 us, a chain of latencies (the
 // plan of the split 1.8 us, first data 3 us, one tile 0.5 us, adding the parts 1.2 us, the join 3).
 //
 //   bf16  S^T = K Q^T and O^T += V^T P^T by m16n8k16 products: the tokens (then the head
@@ -242,9 +243,9 @@ struct PaShape {
   static_assert(CH == 8 || CH == 16 || CH == 32, "whole rows per copy");
 };
 
-// A softmax weight w > 0 as three numbers >= 0 whose upper 16 bits, as bf16, add up to it: eight bits
-// of the mantissa each, cut off and not rounded, so that none is negative.  A part that would be
-// zero is w 2^-30 instead, which changes the sum by less than its rounding: with all three above
+// A softmax weight w > 0 as three numbers >= 0 whose upper 16 bits, as bf16, add up to it: eight
+// bits of the mantissa each, cut off and not rounded, so that none is negative.  A part that would
+// be zero is w 2^-30 instead, which changes the sum by less than its rounding: with all three above
 // zero an infinite value times the weight is that infinity (a weight from 2^-96 on, below which the
 // small part has no normal bf16), where parts of both signs or zero would give NaN.
 __device__ __forceinline__ float upper16(float x) {
@@ -314,9 +315,9 @@ struct PaWarp<__nv_bfloat16, D, GM> {
       for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], a, q[nb][k][0], q[nb][k][1]);
     }
     const bool see0 = (mask >> (lane / 4)) & 1, see1 = (mask >> (lane / 4 + 8)) & 1;
-    // The weights as three bf16 each, all 24 bits of them.  (One alone would add as much error as the
-    // rounding of the output, two leave 16 bits.  Three cost nothing: 64 ragged rows 181 us with two
-    // or three.)
+    // The weights as three bf16 each, all 24 bits of them.  (One alone would add as much error as
+    // the rounding of the output, two leave 16 bits.  Three cost nothing: 64 ragged rows 181 us with
+    // two or three.)
     uint32_t p[NB][3][2];
     float f[NB][2];
 #pragma unroll

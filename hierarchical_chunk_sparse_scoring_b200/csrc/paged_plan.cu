@@ -8,8 +8,10 @@
 // itself (8192 sequences at most, in shared memory), then takes its share of the tokens and pages.
 // Where the new lengths overwrite the old ones the CTAs are one cluster of up to eight, whose
 // barrier lies between reading and writing them (no second launch, no counter in the workspace);
-// else there are as many as the tokens occupy, four tokens a thread together (53 sequences, 131072
-// tokens: 5.4 us; 24.8 us with eight CTAs taking a token at a time; 256 decoding sequences: 5.0 us).
+// else there are as many as the tokens occupy, up to one per SM.  Threads take four tokens together
+// once the tokens outnumber them: past 8192 in place, past 151552 otherwise.  (53 sequences, 131072
+// tokens: 5.2 us, a token a thread; in place 17 us, with a token at a time 24.8 us.  256 decoding
+// sequences: 4.2 us, in place 5.3 us.)
 #include <cooperative_groups.h>
 
 #include "block_scan.cuh"
@@ -23,7 +25,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCluster = 8;          // portable cluster size
-constexpr int kPlanBatch = 4;            // tokens a thread works on together
+constexpr int kPlanBatch = 4;            // tokens a thread works on together, if it has them
 constexpr int kPlanCtas = 148;
 
 // Last b with off[b] <= x (off ascending, off[0] = 0 <= x).

@@ -27,7 +27,8 @@
  *   unit_lse, lse       [B, Hq,  N_q, K+1] / [B, Hq, N_q] fp32
  *
  * Ownership and errors.  The caller owns every buffer, including the workspace; the library
- * allocates no device memory and keeps no state between calls.  Arguments are checked on the
+ * allocates no device memory and keeps no state between calls (but the constants of each device,
+ * looked up once).  Arguments are checked on the
  * host before anything is launched: a bad argument returns an error with nothing written.
  * Otherwise the call is asynchronous on `stream` and returns HILS_ERR_CUDA if a launch fails.
  * Kernels that wait on on-chip barriers give up after a bounded number of polls and record
@@ -227,13 +228,15 @@ hils_status hils_hope_rotate(const hils_params* p, const hils_prologue_params* c
  * Rotary positions.  The first rot_dim dimensions of a head are rot_dim / 2 pairs: pair m is the
  * dimensions (m, m + rot_dim/2) in the half layout and (2m, 2m + 1) in the interleaved one.  At
  * position p a pair (a, b) becomes mscale (a cos t - b sin t, a sin t + b cos t) with
- * t = p freq[m] radians, reduced in fp64; the other dimensions pass unchanged.  hils_rope_init
+ * t = p freq[m] radians, kept as a 64-bit fraction of a turn, so that far positions lose nothing;
+ * the other dimensions pass unchanged.  hils_rope_init
  * fills freq with theta_m = base^(-2m/rot_dim) under one of these rules:
  *   PLAIN   theta_m.
  *   LINEAR  theta_m / factor (positions interpolated to a context factor times as long).
  *   NTK     the base becomes base factor^(rot_dim/(rot_dim - 2)): the slowest pair is slowed by
  *           factor, the fastest keeps its rate.
- *   YARN    (Peng et al. 2023, "YaRN", section 3.2) by the turns r = train_len theta_m / (2 pi) a
+ *   YARN    (Peng et al. 2023, "YaRN", section 3.2; a model whose ramp runs over the pair's index
+ *           instead brings its own freq) by the turns r = train_len theta_m / (2 pi) a
  *           pair makes over the trained length: g theta_m + (1 - g) theta_m / factor with
  *           g = (r - beta_slow) / (beta_fast - beta_slow) clamped to [0, 1];
  *           mscale = 0.1 ln(factor) + 1.
